@@ -361,6 +361,111 @@ int nvfp4_moe_topk(const float *logits, int64_t T, int E, int k, int scoring, in
 int nvfp4_moe_topk_shared(const float *logits, int64_t T, int E, int k, int scoring, int num_shared,
                           int32_t *topk_ids, float *topk_weights, void *stream);
 
+/* ---- operators around the routed block (no counterpart on the pages) ---- */
+
+/* Residual addition + RMS norm with an optional quantised output, the step in
+ * front of the router, the MoE block and the projections.  Per row of H:
+ *   h    = bf16(x + residual)      (x itself without a residual), stored to
+ *          residual_out; the norm reads the rounded h
+ *   rstd = fp32(1 / sqrt(sum(h^2) / H + eps)), the sum in 64 bits
+ *   y    = (h * rstd) * weight in fp32, each product rounded to nearest;
+ *          stored as bf16
+ *   NVFP4_QUANT_NVFP4: codes [T, H/2] and scales as nvfp4_quantize(y, gs)
+ *          writes them, byte for byte (scale_layout NVFP4_SCALES_ROWMAJOR:
+ *          what nvfp4_moe_forward_quantized takes; NVFP4_SCALES_MMA, H % 64
+ *          == 0: what nvfp4_gemm takes; pad rows of the last 128-row block
+ *          are not written)
+ *   NVFP4_QUANT_E4M3: codes [T, H] E4M3 bytes and scales float
+ *          [T, ceil(H/128)], from the fp32 y (not its bf16 rounding): per 128
+ *          columns a = max|y|, scale = a / 448, r = a == 0 ? 0 : 448 / a,
+ *          code = E4M3(y * r) (nearest even); value = code * scale
+ * The results do not depend on T, on a row's place in the batch or on the
+ * launch shape.  Strides are in elements; rows may be strided (ld >= H).
+ * Aliases: residual_out may be residual or x, and y may be x or residual
+ * (same pointer and same stride), nothing else may overlap.
+ * Constraints: T >= 0 (0 launches nothing; pointers may then be NULL),
+ * H % 16 == 0, H <= 32768, eps >= 0, strides % 8 == 0, x / residual /
+ * residual_out / weight / y / codes 16-byte aligned, scales 4-byte aligned.
+ * Inputs must be finite (a row with infinities or NaN spoils that row only). */
+#define NVFP4_QUANT_NONE  0
+#define NVFP4_QUANT_NVFP4 1
+#define NVFP4_QUANT_E4M3  2
+typedef struct {
+    const uint16_t *x;            /* [T, ldx] bf16                                    */
+    const uint16_t *residual;     /* [T, ldr] bf16, or NULL: no addition              */
+    const uint16_t *weight;       /* [H] bf16                                         */
+    int64_t T, H, ldx, ldr, ldro, ldy;
+    double eps;
+    uint16_t *residual_out;       /* [T, ldro] bf16; given exactly when residual is   */
+    uint16_t *y;                  /* [T, ldy] bf16, or NULL with a quantised output   */
+    int32_t quant, scale_layout;
+    const float *gs;              /* device [1], NVFP4: the global scale (warmup)     */
+    uint8_t *codes;
+    void *scales;
+} nvfp4_norm_args;
+int nvfp4_add_rmsnorm(const nvfp4_norm_args *args, void *stream);
+
+/* Products of a few bf16 rows with NVFP4 weights, the few-token companion of
+ * nvfp4_gemm on the same weights (no quantisation of the activations):
+ *   out[m, n] = bf16( sum_k x[m, k] * e2m1(b_codes[n, k]) * e4m3(b_scales[n, k/16]) / b_gs[s] )
+ * with n in segment s; products and sums in fp32, one rounding to bf16; each
+ * output is one sum in a fixed order, so repeated calls give identical
+ * results.  x [M, ldx] bf16, ldx >= K, ldx % 8 == 0; b_codes [N, K/2];
+ * b_scales NVFP4_SCALES_MMA; b_gs device [nseg]; seg_end HOST [nseg],
+ * increasing column ends of the segments, the last equal to N (any ends);
+ * out [M, ldo] bf16, ldo >= N; only the [M, N] window is written.
+ * Constraints: 0 <= M <= 16 (0 launches nothing; x and out may then be NULL),
+ * N >= 1, K % 64 == 0, K <= 1 << 20, 1 <= nseg <= 4; x, b_codes, b_scales
+ * 16-byte aligned.  Inputs must be finite (a row of x that is not spoils that
+ * row of out only). */
+int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
+               const uint8_t *b_codes, const uint8_t *b_scales, const float *b_gs,
+               const int64_t *seg_end, int nseg, int64_t N, int64_t K,
+               uint16_t *out, int64_t ldo, void *stream);
+
+/* Load statistics and balance loss of the router, per sequence.  logits
+ * [T, E] fp32 and topk_ids [T, ld_ids] as nvfp4_moe_topk reads and writes them
+ * (the first k of each row; ld_ids > k: e.g. the rows of
+ * nvfp4_moe_topk_shared, whose shared slots are not counted).  An id outside
+ * [0, E) is a skipped slot; a token whose k slots are all skipped is padding:
+ * its logits are not read and it counts nowhere.  seq_offsets: device int32
+ * [S + 1], non-decreasing in [0, T]; sequence s is the tokens
+ * [seq_offsets[s], seq_offsets[s+1]), tokens outside every sequence are
+ * ignored; NULL: one sequence of all T tokens (S = 1).  With p = softmax(l)
+ * (NVFP4_SCORING_SOFTMAX) or sigmoid(l) / sum sigmoid(l) (.._SIGMOID) over all
+ * E, and per sequence
+ *   counts [S, E] int32  slots of each expert
+ *   tokens [S] int32     n, the tokens that are not padding
+ *   probs  [S, E] fp32   P[e] = sum over those tokens of p[t, e]
+ *   loss   [S] fp32      E / (k n^2) * sum_e counts[e] * P[e]   (0 when n = 0;
+ *                        1 at perfect balance; callers weight and add them)
+ * A logit of -inf has p = 0 (a row of -inf alone: p = 0 everywhere); logits
+ * must not be NaN or +inf.  Sums are fp32 within a chunk of tokens and 64 bits
+ * over the chunks, in a fixed order.  The workspace (caller-owned,
+ * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
+ * scratch: calls sharing one must not overlap on the device.
+ * 1 <= k <= min(E, 32), E <= 1024, S >= 1, T >= 0 (T = 0: logits and topk_ids
+ * may be NULL; zeros are written).  Two launches. */
+size_t nvfp4_moe_balance_workspace_size(int64_t T, int64_t S, int E);
+int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_ids, int64_t T, int E, int k,
+                      const int32_t *seq_offsets, int64_t S, int scoring,
+                      int32_t *counts, int32_t *tokens, float *probs, float *loss,
+                      void *workspace, size_t ws_bytes, void *stream);
+
+/* Gradient with respect to the logits of
+ *   sum_s grad_loss[s] * loss[s]  +  sum_{t,j} grad_weights[t, j] * topk_weights[t, j]
+ * with the loss of nvfp4_moe_balance (counts and tokens as it wrote them; the
+ * counts are constants of the gradient, as ids are) and topk_weights the
+ * renormalised weights of nvfp4_moe_topk over the row's slots that are not
+ * skipped.  grad_loss [S] fp32; grad_weights [T, k] fp32 or NULL (no second
+ * part); grad_logits [T, E] fp32, every row written: rows of padding and of
+ * tokens outside every sequence are 0.  Slots naming one expert twice add up.
+ * Arguments and limits as for nvfp4_moe_balance.  One launch. */
+int nvfp4_moe_balance_backward(const float *logits, const int32_t *topk_ids, int64_t ld_ids, int64_t T, int E, int k,
+                               const int32_t *seq_offsets, int64_t S, int scoring,
+                               const int32_t *counts, const int32_t *tokens, const float *grad_loss,
+                               const float *grad_weights, float *grad_logits, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

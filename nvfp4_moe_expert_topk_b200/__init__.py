@@ -20,11 +20,15 @@ __all__ = [
     "nvfp4_moe_calibrate", "nvfp4_moe_route_debug", "nvfp4_moe_workspace_region",
     "nvfp4_moe_get_error", "nvfp4_moe_topk", "nvfp4_moe_topk_shared", "NVFP4_SCORING_SOFTMAX",
     "NVFP4_SCORING_SIGMOID", "nvfp4_fp4_mma_ceiling", "nvfp4_tma_stream_ceiling", "nvfp4_moe_plan", "nvfp4_amax", "nvfp4_debug_bounded_wait",
-    "MoeArgs",
+    "MoeArgs", "NVFP4_QUANT_NONE", "NVFP4_QUANT_NVFP4", "NVFP4_QUANT_E4M3", "nvfp4_add_rmsnorm", "nvfp4_gemv",
+    "nvfp4_moe_balance_workspace_size", "nvfp4_moe_balance", "nvfp4_moe_balance_backward", "NormArgs",
 ]
 
 NVFP4_SCALES_ROWMAJOR = 0
 NVFP4_SCALES_MMA = 1
+NVFP4_QUANT_NONE = 0
+NVFP4_QUANT_NVFP4 = 1
+NVFP4_QUANT_E4M3 = 2
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
 
 _lib = None
@@ -45,6 +49,18 @@ class MoeArgs(ctypes.Structure):
         ("w13_codes", ctypes.c_void_p), ("w13_scales", ctypes.c_void_p), ("w13_gs", ctypes.c_void_p),
         ("w2_codes", ctypes.c_void_p), ("w2_scales", ctypes.c_void_p), ("w2_gs", ctypes.c_void_p),
         ("inter_gs", ctypes.c_void_p), ("out", ctypes.c_void_p),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of nvfp4_norm_args."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("T", ctypes.c_int64), ("H", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+        ("ldro", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_double),
+        ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("quant", ctypes.c_int32), ("scale_layout", ctypes.c_int32),
+        ("gs", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
     ]
 
 
@@ -85,6 +101,12 @@ def lib():
         L.nvfp4_tma_stream_ceiling.argtypes = [P, i64, i64, i64, i32, P, P]
         L.nvfp4_moe_plan.argtypes = [i64, i32, i32, i64, i64, ctypes.POINTER(ctypes.c_int32),
                                      ctypes.POINTER(ctypes.c_int32)]
+        L.nvfp4_add_rmsnorm.argtypes = [ctypes.POINTER(NormArgs), P]
+        L.nvfp4_gemv.argtypes = [P, i64, i64, P, P, P, ctypes.POINTER(i64), i32, i64, i64, P, i64, P]
+        L.nvfp4_moe_balance_workspace_size.argtypes = [i64, i64, i32]
+        L.nvfp4_moe_balance_workspace_size.restype = ctypes.c_size_t
+        L.nvfp4_moe_balance.argtypes = [P, P, i64, i64, i32, i32, P, i64, i32, P, P, P, P, P, ctypes.c_size_t, P]
+        L.nvfp4_moe_balance_backward.argtypes = [P, P, i64, i64, i32, i32, P, i64, i32, P, P, P, P, P, P]
         _lib = L
     return _lib
 
@@ -329,3 +351,195 @@ def nvfp4_debug_bounded_wait(flag, target, err, stream=None):
     if the wait gives up (after 2 s)."""
     _check(lib().nvfp4_debug_bounded_wait(_dev(flag, "flag", torch.int32), target, _dev(err, "err", torch.int32),
                                           _stream(stream)), "nvfp4_debug_bounded_wait")
+
+
+# ---- operators around the routed block.  Single-token calls of these take a
+# few microseconds on the device, so their marshalling is kept short: pointers
+# travel as plain integers, every tensor's device is compared once, and the
+# launch goes to the device of the tensors (which need not be the current one).
+def _on(dev, t, name, dtype):
+    """Data pointer of a contiguous tensor on CUDA device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required" if t is None else f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_on(dev, t, name, shape):
+    """(data pointer, row stride) of a bf16 matrix whose rows may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required" if t is None else f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    if shape[0] <= 1 or shape[1] == 0:
+        ld = max(ld, (shape[1] + 7) // 8 * 8)      # the stride of a single row is not used
+        ld += -ld % 8
+    return t.data_ptr(), ld
+
+
+def _first(t, name):
+    """The CUDA device index the call runs on: that of its first tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name} must be a CUDA tensor" if t is not None else f"{name} is required")
+    return t.get_device()
+
+
+def _elements(t, name, n):
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
+
+
+def _run(dev, stream, where, call, *args):
+    """call(*args, stream) with `dev` current, on `stream` or the device's
+    current stream."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+        raw = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        st = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, raw)
+    if st != 0:
+        raise Nvfp4Error(st, where)
+
+
+def nvfp4_add_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, quant=NVFP4_QUANT_NONE, gs=None,
+                      codes=None, scales=None, scale_layout=NVFP4_SCALES_ROWMAJOR, stream=None):
+    """h = bf16(x + residual) -> residual_out; y = bf16(RMSnorm(h) * weight),
+    and optionally the row quantised (see include/nvfp4moe.h): x, residual,
+    residual_out, y bf16 [T, H] (rows may be strided; residual_out may be
+    residual or x, y may be x or residual), weight bf16 [H];
+    NVFP4_QUANT_NVFP4: gs float32 [1], codes uint8 [T, H/2], scales uint8
+    (nvfp4_scales_bytes(T, H, scale_layout) bytes); NVFP4_QUANT_E4M3: codes
+    uint8 or float8_e4m3fn [T, H], scales float32 [T, ceil(H/128)]."""
+    dev = _first(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, H], got {list(shape)}")
+    T, H = shape
+    a = NormArgs()
+    a.T, a.H, a.eps, a.quant, a.scale_layout = T, H, eps, quant, scale_layout
+    a.x, a.ldx = _rows_on(dev, x, "x", shape)
+    a.weight = _on(dev, weight, "weight", torch.bfloat16)
+    _elements(weight, "weight", H)
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out come together")
+    if residual is not None:
+        a.residual, a.ldr = _rows_on(dev, residual, "residual", shape)
+        a.residual_out, a.ldro = _rows_on(dev, residual_out, "residual_out", shape)
+    if y is not None:
+        a.y, a.ldy = _rows_on(dev, y, "y", shape)
+    elif quant == NVFP4_QUANT_NONE:
+        raise ValueError("y is required without a quantised output")
+    if quant == NVFP4_QUANT_NVFP4:
+        a.gs = _on(dev, gs, "gs", torch.float32)
+        a.codes = _on(dev, codes, "codes", torch.uint8)
+        a.scales = _on(dev, scales, "scales", torch.uint8)
+        _elements(gs, "gs", 1)
+        _elements(codes, "codes", T * (H // 2))
+        need = nvfp4_scales_bytes(T, H, scale_layout)
+        if scales.numel() < need:
+            raise ValueError(f"scales must hold {need} bytes, got {scales.numel()}")
+    elif quant == NVFP4_QUANT_E4M3:
+        if codes is not None and codes.dtype == torch.float8_e4m3fn:
+            a.codes = _on(dev, codes, "codes", torch.float8_e4m3fn)
+        else:
+            a.codes = _on(dev, codes, "codes", torch.uint8)
+        a.scales = _on(dev, scales, "scales", torch.float32)
+        _elements(codes, "codes", T * H)
+        _elements(scales, "scales", T * ((H + 127) // 128))
+    _run(dev, stream, "nvfp4_add_rmsnorm", lib().nvfp4_add_rmsnorm, a)
+
+
+def nvfp4_gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
+    """out bf16 [M, N] = x bf16 [M, K] (M <= 16, not quantised) x B [N, K]^T
+    in NVFP4 (scales in the MMA layout, b_gs one global scale per segment of
+    rows ending at seg_end); rows of x and out may be strided."""
+    dev = _first(x, "x")
+    M, K = x.shape
+    N = b_codes.shape[0]
+    px, ldx = _rows_on(dev, x, "x", x.shape)
+    po, ldo = _rows_on(dev, out, "out", (M, N))
+    pc = _on(dev, b_codes, "b_codes", torch.uint8)
+    _elements(b_codes, "b_codes", N * (K // 2))
+    ps = _on(dev, b_scales, "b_scales", torch.uint8)
+    if b_scales.numel() < (N + 127) // 128 * 128 * (K // 16):
+        raise ValueError(f"b_scales must hold {nvfp4_scales_bytes(N, K, NVFP4_SCALES_MMA)} bytes, "
+                         f"got {b_scales.numel()}")
+    pg = _on(dev, b_gs, "b_gs", torch.float32)
+    nseg = len(seg_end)
+    _elements(b_gs, "b_gs", nseg)
+    _run(dev, stream, "nvfp4_gemv", lib().nvfp4_gemv, px, M, ldx, pc, ps, pg, (ctypes.c_int64 * nseg)(*seg_end), nseg,
+         N, K, po, ldo)
+
+
+def nvfp4_moe_balance_workspace_size(T, S, E):
+    return int(lib().nvfp4_moe_balance_workspace_size(T, S, E))
+
+
+def _balance_inputs(logits, topk_ids, k, seq_offsets):
+    dev = _first(logits, "logits")
+    T, E = logits.shape
+    pl = _on(dev, logits, "logits", torch.float32)
+    pi = _on(dev, topk_ids, "topk_ids", torch.int32)
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_ids.shape[1] < k:
+        raise ValueError(f"topk_ids must be [{T}, >= {k}], got {list(topk_ids.shape)}")
+    if seq_offsets is None:
+        return dev, pl, pi, topk_ids.shape[1], T, E, None, 1
+    po = _on(dev, seq_offsets, "seq_offsets", torch.int32)
+    return dev, pl, pi, topk_ids.shape[1], T, E, po, seq_offsets.numel() - 1
+
+
+def nvfp4_moe_balance(logits, topk_ids, k, counts, tokens, probs, loss, workspace, seq_offsets=None,
+                      scoring=NVFP4_SCORING_SOFTMAX, stream=None):
+    """Per-expert load and balance loss of each sequence (see
+    include/nvfp4moe.h): logits [T, E] fp32 and topk_ids [T, >= k] int32 of the
+    router -> counts [S, E] int32, tokens [S] int32, probs [S, E] fp32, loss
+    [S] fp32; seq_offsets int32 [S + 1] (None: one sequence); workspace: uint8,
+    nvfp4_moe_balance_workspace_size(T, S, E) bytes."""
+    dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
+    pc, pt = _on(dev, counts, "counts", torch.int32), _on(dev, tokens, "tokens", torch.int32)
+    pp, ps = _on(dev, probs, "probs", torch.float32), _on(dev, loss, "loss", torch.float32)
+    pw = _on(dev, workspace, "workspace", torch.uint8)
+    _elements(counts, "counts", S * E)
+    _elements(tokens, "tokens", S)
+    _elements(probs, "probs", S * E)
+    _elements(loss, "loss", S)
+    _run(dev, stream, "nvfp4_moe_balance", lib().nvfp4_moe_balance, pl, pi, ld, T, E, k, po, S, scoring, pc, pt, pp,
+         ps, pw, workspace.numel())
+
+
+def nvfp4_moe_balance_backward(logits, topk_ids, k, counts, tokens, grad_loss, grad_logits, grad_weights=None,
+                               seq_offsets=None, scoring=NVFP4_SCORING_SOFTMAX, stream=None):
+    """grad_logits [T, E] fp32 = gradient of sum_s grad_loss[s] * loss[s] (and
+    of sum grad_weights * topk_weights when grad_weights [T, k] is given) with
+    respect to the logits; counts and tokens as nvfp4_moe_balance wrote them."""
+    dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
+    pc, pt = _on(dev, counts, "counts", torch.int32), _on(dev, tokens, "tokens", torch.int32)
+    pg, pd = _on(dev, grad_loss, "grad_loss", torch.float32), _on(dev, grad_logits, "grad_logits", torch.float32)
+    _elements(counts, "counts", S * E)
+    _elements(tokens, "tokens", S)
+    _elements(grad_loss, "grad_loss", S)
+    _elements(grad_logits, "grad_logits", T * E)
+    pw = None
+    if grad_weights is not None:
+        pw = _on(dev, grad_weights, "grad_weights", torch.float32)
+        _elements(grad_weights, "grad_weights", T * k)
+    _run(dev, stream, "nvfp4_moe_balance_backward", lib().nvfp4_moe_balance_backward, pl, pi, ld, T, E, k, po, S,
+         scoring, pc, pt, pg, pw, pd)

@@ -432,6 +432,11 @@ int nvfp4::moe_args_status(const nvfp4_moe_args *args, bool need_out)
     return check_moe_args(args, need_out);
 }
 
+int nvfp4::device_status(int *num_sms)
+{
+    return device_check(num_sms);
+}
+
 extern "C" {
 
 const char *nvfp4_status_string(int status)

@@ -39,6 +39,10 @@ cudaError_t ensure_smem_limit(const void *kernel, int bytes, unsigned long long 
 // 16-byte alignment), as a status code; no device work (api.cu).
 int moe_args_status(const nvfp4_moe_args *args, bool need_out);
 
+// NVFP4_OK when the current device is sm_100 (its SM count in *num_sms when
+// not null), else the status to return (api.cu).
+int device_status(int *num_sms);
+
 // Arguments of the persistent block-scaled FP4 GEMM engine (gemm.cu).
 struct GemmArgs {
     // scale factors, NVFP4_SCALES_MMA layout: one 128-row block = (K/64) atoms of 512 bytes
@@ -180,5 +184,59 @@ cudaError_t launch_tma_stream(const CUtensorMap &map, int64_t rows, int64_t row_
                               int stages, int ctas, int32_t *err, cudaStream_t s);
 cudaError_t launch_topk(const float *logits, int64_t T, int E, int k, int ns, int scoring, int32_t *ids,
                         float *weights, cudaStream_t s);
+
+// Residual addition + RMS norm with a quantised output (norm.cu).
+struct NormArgs {
+    const __nv_bfloat16 *x, *residual, *weight;   // residual may be null
+    __nv_bfloat16 *residual_out, *y;              // y may be null; residual_out only with residual
+    int64_t ldx, ldr, ldro, ldy;
+    int64_t T;
+    int nb;                   // H / 16
+    double eps;
+    int quant, layout;        // NVFP4_QUANT_*, NVFP4_SCALES_*
+    const float *gs;
+    uint8_t *codes;
+    void *scales;
+};
+constexpr int kNormMaxCols = 32768;
+cudaError_t launch_add_rmsnorm(const NormArgs &args, int num_sms, cudaStream_t s);
+
+// A few bf16 rows times NVFP4 weights (gemv.cu).
+constexpr int kGemvMaxRows = 16;
+struct GemvArgs {
+    const __nv_bfloat16 *x;
+    int64_t M, ldx;
+    const uint8_t *codes, *scales;                // [N, K/2]; NVFP4_SCALES_MMA
+    const float *gs;
+    int nseg;
+    int64_t seg_end[4];
+    int64_t N, K;
+    __nv_bfloat16 *out;
+    int64_t ldo;
+};
+cudaError_t launch_gemv(const GemvArgs &args, int num_sms, cudaStream_t s);
+
+// Router load statistics, balance loss and gradient (balance.cu).
+struct BalanceArgs {
+    const float *logits;
+    const int32_t *ids;
+    int64_t ld_ids;
+    int k;
+    int64_t T;
+    int E, S;
+    const int32_t *offsets;   // [S + 1], or null: one sequence of T tokens
+    int scoring;
+    int chunk;                // tokens per chunk slot
+    int32_t *counts, *tokens;
+    float *probs, *loss;
+    float *part_p;            // per chunk slot: [E] sums, [E] counts, tokens
+    int32_t *part_c, *part_n;
+    const float *grad_loss, *grad_weights;
+    float *grad_logits;
+};
+int balance_chunk(int64_t T);
+int64_t balance_slots(int64_t T, int64_t S);
+cudaError_t launch_balance(const BalanceArgs &args, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs &args, cudaStream_t s);
 
 } // namespace nvfp4
