@@ -215,6 +215,9 @@ struct GemvArgs {
     int64_t ldo;
 };
 cudaError_t launch_gemv(const GemvArgs &args, int num_sms, cudaStream_t s);
+// The same with a given split: row tiles and k slices per block, blocks per
+// cluster (each of them a further split of k).
+cudaError_t launch_gemv_as(const GemvArgs &args, int tiles, int slices, int cluster, cudaStream_t s);
 
 // Router load statistics, balance loss and gradient (balance.cu).
 struct BalanceArgs {
