@@ -437,6 +437,29 @@ int nvfp4::device_status(int *num_sms)
     return device_check(num_sms);
 }
 
+int nvfp4::code_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols_bytes, int box_rows)
+{
+    return make_code_map(map, base, rows, cols_bytes, box_rows);
+}
+
+int nvfp4::byte_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, bool swizzle128)
+{
+    cuuint64_t d[3] = {0, 0, 0}, st[2] = {0, 0};
+    cuuint32_t b[3] = {0, 0, 0}, one[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i > 0)
+            st[i - 1] = strides[i - 1];
+    }
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+                                const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 extern "C" {
 
 const char *nvfp4_status_string(int status)

@@ -118,7 +118,8 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *b_codes
         return NVFP4_ERR_INVALID_ARG;
     if (M > 0 && (x == nullptr || out == nullptr || ldx < K || ldo < N))
         return NVFP4_ERR_INVALID_ARG;
-    if (M > kGemvMaxRows || K % 64 != 0 || K > (1LL << 20) || N >= (1LL << 31) - 1024 || nseg > 4)
+    if (M > kGemvMaxRows || K % 64 != 0 || K > (1LL << 20) || N > (1LL << 30) || nseg > 4 ||
+        (N + 127) / 128 * (K / 64) >= (1LL << 31))
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
     int64_t prev = 0;
     for (int i = 0; i < nseg; ++i) {

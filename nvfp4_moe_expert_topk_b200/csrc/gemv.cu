@@ -3,30 +3,40 @@
 //   out[m, n] = bf16( sum_k x[m, k] * e2m1(code[n, k]) * e4m3(scale[n, k / 16]) / gs[segment of n] )
 // The activations are not quantised.
 //
-// What bounds it: the weights are read once (9/16 byte each) and every one has
-// to be turned from a nibble and a scale byte into a tensor-core operand.  A
-// weight times its scale has 6 significant bits, so it is exact in bf16, and
-// bf16 x bf16 products are exact in the fp32 accumulators of
-// mma.sync.m16n8k16: the weights are its 16-row operand, the x rows (up to 8,
-// or two sets of 8) its 8 columns.  (mma.sync and not tcgen05: the operand is
+// What bounds it: the weights are read once (9/16 byte each), and every one
+// has to be turned from a nibble and a scale byte into a tensor-core operand.
+// A weight times its scale has 6 significant bits and at most 2688 in value,
+// so it is exact in f16: cvt.f16x2.e2m1x2 and one packed product per two
+// weights, half the instructions that making bf16 operands with shifts and
+// masks takes (measured: 64 lanes a clock and SM for the conversion as for
+// the product).  The products run on mma.sync.m16n8k16 (f16, fp32
+// accumulators), the weights as its 16-row operand, the x rows (up to 8, or
+// two sets of 8) as its columns.  (mma.sync and not tcgen05: the operand is
 // made in registers, and at 8 or 16 columns the tensor pipe idles either way.)
 //
-// Decoding.  A nibble s.ee.m placed at bits 15 | 8..6 of a bf16 is the value
-// e2m1 * 2^-126 (subnormal where ee = 0), and an E4M3 byte at bits 11..4 is
-// e4m3 * 2^-120, so both conversions are shifts and masks and one packed
-// product joins them: (e2m1 * 2^-126) * (e4m3 * 2^118) = weight * 2^-8, exact.
-// Two nibbles 16 bits apart are handled at once, which pairs elements i and
-// i + 4 of a group of eight; x is paired the same way (a permutation of k
-// inside a group does not change the sum).
+// x in f16: each row's piece of k that a warp sums is scaled by a power of two
+// that brings its largest magnitude into [2^14, 2^15); f16 then holds a bf16
+// value exactly down to 2^-31 of that largest one, and rounds what is smaller
+// to within 2^-39 of it -- 2^15 below the fp32 rounding of the largest
+// product.  The power of two is undone in fp32.
 //
-// Tiles.  A warp owns 32 rows, 8 consecutive ones g in each 32-row quarter of
-// a 128-row scale block: the four rows' scales of 64 columns then are 16
-// consecutive bytes of the layout.  Per step of 128 columns lane (g, t) loads
-// 16 bytes of codes of each of its rows (two scale blocks per row) and one
-// 16-byte piece of scales; the next step's loads are issued before the current
-// step is used.  The steps of a row tile are split over the warps of a block
-// and over the blocks of a cluster, whose partial sums meet in shared memory
-// in a fixed order.
+// Tiles.  A warp works on row tiles of 32 rows, 8 consecutive ones g in each
+// 32-row quarter of a 128-row scale block: the four rows' scales of 64 columns
+// then are 16 consecutive bytes of the layout.  Per step of 256 columns one
+// lane brings the tile's codes (a TMA box of 4 quarters x 8 rows x 128 bytes)
+// and its scales (4 atoms x 128 bytes) into the warp's own ring in shared
+// memory, on into the next tile (the same loads with cp.async by every lane
+// stopped at 4 TB/s, from L2 too).  Lane (g, t) owns columns 64 t .. 64 t + 63 of the step,
+// in two halves of 32: 16-byte pieces 2 t + h of its rows, which the 128-byte
+// swizzle of the boxes puts on distinct banks for every eight lanes, and the
+// scale word of atom t.  (Which k goes to which place of the instruction does
+// not matter as long as weights and x agree.)
+//
+// Blocks are persistent (one per SM): each converts its piece of x once, in
+// the order its lanes read it, and walks over row tiles.  k is split over the
+// blocks of a cluster and over the `slices` warps of a tile; partial sums meet
+// in shared memory in a fixed order.  Every wait on a copy is bounded: a warp
+// that gives up stops loading and ends with sums of what it has.
 #include <algorithm>
 
 #include "internal.h"
@@ -36,17 +46,7 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kStep = 128;               // columns per step
-
-// Nibble pairs (i, i + 4) of eight packed codes as bf16 pairs scaled by 2^-126.
-__device__ __forceinline__ void e2m1_pairs(uint32_t q, uint32_t (&p)[4])
-{
-    const uint32_t r = q >> 8;
-    p[0] = ((q << 6) & 0x01C001C0u) | ((q << 12) & 0x80008000u);
-    p[1] = ((q << 2) & 0x01C001C0u) | ((q << 8) & 0x80008000u);
-    p[2] = ((r << 6) & 0x01C001C0u) | ((r << 12) & 0x80008000u);
-    p[3] = ((r << 2) & 0x01C001C0u) | ((r << 8) & 0x80008000u);
-}
+constexpr int kStep = 256;               // columns per step: 128 bytes of codes per row
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
@@ -55,223 +55,507 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return d;
 }
 
-// E4M3 byte `byte` of a word, twice, as bf16 * 2^118.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t word, int byte)
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 {
-    constexpr uint32_t k2p119 = 0x7B007B00u;
-    const uint32_t v = __byte_perm(word, 0u, 0x4040u | byte | byte << 8) << 4;
-    return mul_bf16x2(mul_bf16x2(v, k2p119), k2p119);
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1)
+// Eight packed codes -> four f16 pairs (elements 2 i, 2 i + 1), exact.
+__device__ __forceinline__ void e2m1_pairs(uint32_t q, uint32_t (&p)[4])
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+        : "r"(q));
+}
+
+// Two E4M3 bytes (the low half of v) -> two f16 pairs, each scale twice.
+__device__ __forceinline__ void scale_pairs(uint32_t v, uint32_t (&s)[2])
+{
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(v));
+    s[0] = __byte_perm(h, 0u, 0x1010);
+    s[1] = __byte_perm(h, 0u, 0x3232);
+}
+
+// bf16 pair times a power of two (both halves of p2) -> f16 pair.
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t x, uint32_t p2)
+{
+    const uint32_t v = mul_bf16x2(x, p2);
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+        : "=r"(d)
+        : "f"(__uint_as_float(v & 0xFFFF0000u)), "f"(__uint_as_float(v << 16)));
+    return d;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One step's weights of a lane: 16 bytes of codes of its four rows, and the
-// four rows' scales of the 64 columns that hold its two blocks.
-struct WStep {
-    uint4 c[4];
-    uint4 s;
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+constexpr int kCodeStage = 4096, kScaleStage = 512;            // bytes per ring stage of a warp
+constexpr int kMaxWarps = 16, kMaxDepth = 4;
+constexpr int kKeep = 4;                           // pieces of x per lane kept from the maximum to the conversion
+
+// A launch's split, and its shared memory in bytes: the rings, the converted x
+// of one panel of k, the partial sums of the tiles' slices and those of the
+// cluster's blocks.
+struct GemvPlan {
+    int groups, slices, cluster;                   // row tiles and k slices at a time per block; blocks per cluster
+    int clusters;                                  // in the grid
+    int depth;                                     // ring stages per warp
+    int panel;                                     // steps of x held at a time
+    int rounds;                                    // tiles per group
+    __host__ __device__ int warps() const { return groups * slices; }
+    __host__ __device__ int codes() const { return warps() * depth * kCodeStage; }
+    __host__ __device__ int ring() const { return codes() + warps() * depth * kScaleStage; }
+    __host__ __device__ int x(int mt) const { return panel * mt * 4096; }
+    __host__ __device__ int red(int mt) const { return slices > 1 ? warps() * mt * 1024 : 0; }
+    __host__ __device__ int owned() const { return (rounds + cluster - 1) / cluster; }
+    __host__ __device__ int sums(int mt) const { return cluster > 1 ? cluster * owned() * groups * mt * 1024 : 0; }
+    __host__ __device__ int total(int mt) const { return ring() + x(mt) + red(mt) + sums(mt); }
 };
+
+// The launch's tensor maps: codes as [N / 32][32][K / 2] (whole blocks of 128
+// rows), codes as [N][K / 2] (the last, partial block), scale atoms as
+// [blocks * K / 64][512].
+struct GemvMaps {
+    CUtensorMap blocks, rows, scales;
+};
+
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                           uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// All threads of the `n` warps that share barrier `id`.
+__device__ __forceinline__ void bar_group(int id, int n)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * n) : "memory");
+}
 
 } // namespace
 
-// blockDim = 32 * row_tiles * slices; gridDim = cluster * row groups.
 template <int MT>
-__global__ void __launch_bounds__(512) gemv_kernel(const GemvArgs a, int slices, int cluster)
+__global__ void __launch_bounds__(32 * kMaxWarps)
+    gemv_kernel(const __grid_constant__ GemvMaps maps, const GemvArgs a, const GemvPlan pl)
 {
-    extern __shared__ float red[];                 // [warps][8 * MT][32]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    extern __shared__ uint8_t sm_raw[];
+    __shared__ uint32_t expo[8 * MT];
+    __shared__ uint64_t bars[kMaxWarps * kMaxDepth];
+    __shared__ float inv_gs[4];
+    __shared__ int never_abort;
+    constexpr int kVals = 8 * MT;                  // sums per lane and row tile
+    // four accumulators in turn, so that an instruction does not wait for the previous one's sums
+    constexpr int kChains = MT == 1 ? 2 : 1;
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = pl.warps();
     const int g = lane >> 2, t = lane & 3;
-    const int tiles = (blockDim.x >> 5) / slices;  // row tiles of this block
-    const int tile = warp / slices, slice = warp - tile * slices;
-    const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-    const int64_t tile_id = static_cast<int64_t>(blockIdx.x / cluster) * tiles + tile;
-    const int64_t row0 = (tile_id >> 2) * 128 + (tile_id & 3) * 8 + g;
-    const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
-    const int part = rank * slices + slice, parts = slices * cluster;
-    const int s0 = static_cast<int>(static_cast<int64_t>(steps) * part / parts);
-    const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / parts);
+    const int group = warp / pl.slices, slice = warp - group * pl.slices;
+    const int cluster = pl.cluster, rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cid = blockIdx.x / cluster;
+    const int K = static_cast<int>(a.K);
+    const int steps = (K + kStep - 1) / kStep;
+    const int b0 = steps * rank / cluster, b1 = steps * (rank + 1) / cluster;       // the block's steps
+    const int full_blocks = static_cast<int>(a.N >> 7);
 
-    const uint8_t *cp[4];
+    if (cluster > 1)
+        cluster_arrive();                          // waited for before the first store to a peer
+    if (threadIdx.x < 8 * MT)
+        expo[threadIdx.x] = 15u;                   // smallest exponent field: both powers of two stay normal
+    uint64_t *bar = bars + warp * kMaxDepth;
+    if (lane == 0) {
+        for (int d = 0; d < pl.depth; ++d)
+            mbar_init(&bar[d], 1);
+        never_abort = 0;
+        fence_mbar_init();
+        if (warp == 0) {
+            tma_prefetch_map(&maps.blocks);
+            tma_prefetch_map(&maps.scales);
+        }
+    }
+    uint8_t *codes_s = sm + warp * pl.depth * kCodeStage;
+    uint8_t *scales_s = sm + pl.codes() + warp * pl.depth * kScaleStage;
+    uint4 *xs = reinterpret_cast<uint4 *>(sm + pl.ring());
+    float *red = reinterpret_cast<float *>(sm + pl.ring() + pl.x(MT)) + group * pl.slices * (kVals * 32) + lane;
+    float *sums = reinterpret_cast<float *>(sm + pl.ring() + pl.x(MT) + pl.red(MT));
+
+    // Tile of round `it` (past the last: rows that do not exist, zeros).
+    auto tile_of = [&](int it) { return (it * pl.clusters + cid) * pl.groups + group; };
+    // Prefetch cursor over (round, step) up to f_end rounds; lane 0 brings one
+    // step into a ring slot; columns past K and rows past N arrive as zeros.
+    int f_it = 0, f_end = 0, f_step = 0, f_slot = 0, first = 0, last = 0;
+    auto fetch = [&]() {
+        if (f_it < f_end && first < last) {
+            if (lane == 0) {
+                const int tile = tile_of(f_it), blk = tile >> 2, row = (tile & 3) * 8;
+                uint64_t *full = &bar[f_slot];
+                uint8_t *dst = codes_s + f_slot * kCodeStage;
+                mbar_arrive_expect_tx(full, kCodeStage + kScaleStage);
+                if (blk < full_blocks)
+                    tma_load_3d(dst, &maps.blocks, f_step * (kStep / 2), row, 4 * blk, full);
+                else
+                    for (int j = 0; j < 4; ++j)
+                        tma_load_2d(dst + 1024 * j, &maps.rows, f_step * (kStep / 2), blk * 128 + row + 32 * j, full);
+                // (atoms past K are the next block's, or zeros past the last: masked when they are used)
+                tma_load_2d(scales_s + f_slot * kScaleStage, &maps.scales, row * 16, blk * (K / 64) + 4 * f_step, full);
+            }
+            if (++f_step == last) {
+                f_step = first;
+                ++f_it;
+            }
+            f_slot = f_slot + 1 == pl.depth ? 0 : f_slot + 1;
+        }
+    };
+
+    // Pieces of x: for each set m of 8 rows, piece i is 8 columns of each lane's
+    // 64 in one step (i / 8, i % 8); warp w takes the pieces w, w + warps, ...
+    auto piece = [&](int m, int p0, int i) -> uint4 {
+        const int row = 8 * m + g, k = (p0 + (i >> 3)) * kStep + 64 * t + 8 * (i & 7);
+        return row < a.M && k < K ? __ldg(reinterpret_cast<const uint4 *>(a.x + row * a.ldx + k))
+                                  : make_uint4(0, 0, 0, 0);
+    };
+    auto put = [&](int m, int i, const uint4 &v, uint32_t p2) {
+        xs[((i >> 2) * (MT * 4) + m * 4 + (i & 3)) * 32 + lane] =
+            make_uint4(to_f16x2(v.x, p2), to_f16x2(v.y, p2), to_f16x2(v.z, p2), to_f16x2(v.w, p2));
+    };
+    // 2^(141 - exponent) in bf16, twice
+    auto power = [&](int m) { return (268u - expo[8 * m + g]) * 0x00800080u; };
+    auto convert = [&](int p0, int n, int from) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)                    // rows past N read row N - 1; their sums are not stored
-        cp[j] = a.codes + min(row0 + 32 * j, a.N - 1) * (a.K / 2) + 16 * t;
-    const uint8_t *sp = a.scales + (min(row0, a.N - 1) >> 7) * (a.K / 64) * 512 + ((tile_id & 3) * 8 + g) * 16;
-    float acc[2][MT][4];
+        for (int m = 0; m < MT; ++m)
+            if (8 * m + g < a.M) {                 // other columns hold anything: their sums are not stored
+                const uint32_t p2 = power(m);
+#pragma unroll 4
+                for (int i = from; i < 8 * n; i += warps)
+                    put(m, i, piece(m, p0, i), p2);
+            }
+    };
+    // this warp's steps of the panel [p0, p0 + n)
+    auto share = [&](int p0, int n) {
+        first = f_step = p0 + n * slice / pl.slices;
+        last = p0 + n * (slice + 1) / pl.slices;
+    };
+
+    const bool whole = b1 - b0 <= pl.panel;        // the block's x stays: the ring runs on from tile to tile
+    __syncwarp();
+    pdl_wait();
+    pdl_trigger();
+    if (whole) {
+        share(b0, b1 - b0);
+        f_end = pl.rounds;
+        for (int d = 0; d < pl.depth; ++d)
+            fetch();
+    }
+    if (threadIdx.x < a.nseg)
+        inv_gs[threadIdx.x] = __fdiv_rn(1.0f, __ldg(a.gs + threadIdx.x));
+    // the largest exponent of each row's piece of k; the first pieces stay in
+    // registers until they are converted
+    uint4 keep[MT][kKeep];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u)
+            keep[m][u] = warp + u * warps < (b1 - b0) * 8 ? piece(m, b0, warp + u * warps) : make_uint4(0, 0, 0, 0);
+    __syncthreads();                               // expo is initialised
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        uint32_t mx = 0;
+        auto top = [&](const uint4 &v) {
+            mx = __vmaxu2(mx, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+            mx = __vmaxu2(mx, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+        };
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u)
+            top(keep[m][u]);
+#pragma unroll 4
+        for (int i = warp + kKeep * warps; i < (b1 - b0) * 8; i += warps)
+            top(piece(m, b0, i));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        mx = max(mx & 0xFFFFu, mx >> 16) >> 7;
+        if (t == 0 && mx > 15u)
+            atomicMax(&expo[8 * m + g], mx);
+    }
+    __syncthreads();
+    if (whole) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[p][m][i] = 0.0f;
-
-    pdl_wait();
-    pdl_trigger();
-    auto load = [&](WStep &w, int step) {
-        const bool on = step < s1 && step * kStep + 32 * t < a.K;
-        const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w.c[j] = on ? __ldg(reinterpret_cast<const uint4 *>(cp[j] + static_cast<int64_t>(step) * (kStep / 2))) : z;
-        w.s = on ? __ldg(reinterpret_cast<const uint4 *>(sp + (2 * static_cast<int64_t>(step) + (t >> 1)) * 512)) : z;
-    };
-    WStep cur, nxt;
-    load(cur, s0);
-    for (int step = s0; step < s1; ++step) {
-        load(nxt, step + 1);
-        uint4 x[MT][4];
-        const int k = step * kStep + 32 * t;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const bool on = 8 * m + g < a.M && k < a.K;
-            const uint4 *xs = reinterpret_cast<const uint4 *>(a.x + (8 * m + g) * a.ldx + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[m][i] = on ? __ldg(xs + i) : make_uint4(0, 0, 0, 0);
-        }
-        const uint32_t sw[4] = {cur.s.x, cur.s.y, cur.s.z, cur.s.w};
-        const int sb = 2 * (t & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {              // eight columns of each lane's 32
-            uint32_t b[MT][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                b[m][0] = __byte_perm(x[m][i].x, x[m][i].z, 0x5410);
-                b[m][1] = __byte_perm(x[m][i].x, x[m][i].z, 0x7632);
-                b[m][2] = __byte_perm(x[m][i].y, x[m][i].w, 0x5410);
-                b[m][3] = __byte_perm(x[m][i].y, x[m][i].w, 0x7632);
-            }
-            uint32_t w[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t q = i == 0 ? cur.c[j].x : i == 1 ? cur.c[j].y : i == 2 ? cur.c[j].z : cur.c[j].w;
-                const uint32_t sc = scale_pair(sw[j], sb + (i >> 1));
-                e2m1_pairs(q, w[j]);
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    w[j][u] = mul_bf16x2(w[j][u], sc);
-            }
-#pragma unroll
-            for (int h = 0; h < 4; h += 2)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        mma_bf16(acc[p][m], w[2 * p][h], w[2 * p + 1][h], w[2 * p][h + 1], w[2 * p + 1][h + 1],
-                                 b[m][h], b[m][h + 1]);
-        }
-        cur = nxt;
+            for (int u = 0; u < kKeep; ++u)
+                if (8 * m + g < a.M && warp + u * warps < (b1 - b0) * 8)
+                    put(m, warp + u * warps, keep[m][u], power(m));
+        convert(b0, b1 - b0, warp + kKeep * warps);
+        __syncthreads();
     }
 
-    // sums over the slices of a block, then over the blocks of the cluster
-    constexpr int kVals = 8 * MT;
-    if (slices > 1 || cluster > 1) {
+    // value v of a lane: its weight row's place in the tile and its x row
+    auto store = [&](int tile, int v, float s) {
+        const int j = 2 * (v / (4 * MT)) + ((v >> 1) & 1), row = 8 * (v / 4 % MT) + 2 * t + (v & 1);
+        const int64_t n = static_cast<int64_t>(tile >> 2) * 128 + (tile & 3) * 8 + g + 32 * j;
+        if (n < a.N && row < a.M) {
+            const int seg = (a.nseg > 1 && n >= a.seg_end[0]) + (a.nseg > 2 && n >= a.seg_end[1]) +
+                            (a.nseg > 3 && n >= a.seg_end[2]);
+            a.out[row * a.ldo + n] = __float2bfloat16_rn(s * inv_gs[seg]);
+        }
+    };
+
+    // undoes the x row's power of two (each block of a cluster has its own)
+    auto unscale = [&](int v, float s) {
+        return s * __uint_as_float((expo[8 * (v / 4 % MT) + 2 * t + (v & 1)] - 14u) << 23);
+    };
+
+    bool peers_up = cluster == 1, ok = true;
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int it = 0; it < pl.rounds; ++it) {
+        float acc[2][MT][kChains][4];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    red[(warp * kVals + (p * MT + m) * 4 + i) * 32 + lane] = acc[p][m][i];
-        __syncthreads();
-        if (slice == 0) {
-#pragma unroll
-            for (int v = 0; v < kVals; ++v) {
-                float s = red[(warp * kVals + v) * 32 + lane];
-                for (int w = 1; w < slices; ++w)
-                    s += red[((warp + w) * kVals + v) * 32 + lane];
-                acc[v / (4 * MT)][v / 4 % MT][v % 4] = s;
-                red[(warp * kVals + v) * 32 + lane] = s;
+                for (int v = 0; v < 4 * kChains; ++v)
+                    acc[p][m][v >> 2][v & 3] = 0.0f;
+        for (int p0 = b0; p0 < b1; p0 += pl.panel) {
+            if (!whole) {                          // x does not fit: panel by panel, again for every tile
+                const int n = min(pl.panel, b1 - p0);
+                __syncthreads();                   // the previous panel of x is read
+                convert(p0, n, warp);
+                __syncthreads();
+                share(p0, n);
+                f_it = it;
+                f_end = it + 1;
+                for (int d = 0; d < pl.depth; ++d)
+                    if (ok)
+                        fetch();
             }
-        }
-        if (cluster > 1) {
-            cluster_sync();
-            if (rank == 0 && slice == 0) {
-                for (int r = 1; r < cluster; ++r) {
-                    const uint32_t peer = map_shared_to_cta(smem_u32(red), r);
+            for (int step = first; step < last && ok; ++step) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &never_abort));
+                if (!ok)
+                    break;
+                const uint8_t *cs = codes_s + slot * kCodeStage + g * 128;
+                uint4 s4 = *reinterpret_cast<const uint4 *>(scales_s + slot * kScaleStage + t * 128 + g * 16);
+                if (step * kStep + 64 * t >= K)
+                    s4 = make_uint4(0, 0, 0, 0);   // scales past K are not loaded
+                const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
+                const uint4 *xp = xs + (step - p0) * (2 * MT * 128) + lane;
 #pragma unroll
-                    for (int v = 0; v < kVals; ++v) {
-                        float s;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(s)
-                                     : "r"(peer + 4u * ((warp * kVals + v) * 32 + lane)));
-                        acc[v / (4 * MT)][v / 4 % MT][v % 4] += s;
+                for (int h = 0; h < 2; ++h) {      // 32 of the lane's 64 columns
+                    uint32_t sc[4][2];
+                    uint4 c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        scale_pairs(h ? sw[j] >> 16 : sw[j], sc[j]);
+                        c[j] = *reinterpret_cast<const uint4 *>(cs + 1024 * j + (((2 * t + h) ^ g) << 4));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // eight of them
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            e2m1_pairs(q == 0 ? c[j].x : q == 1 ? c[j].y : q == 2 ? c[j].z : c[j].w, v[j]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[j][e] = mul_f16x2(v[j][e], sc[j][q >> 1]);
+                        }
+                        uint4 x[MT];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            x[m] = xp[(h * MT + m) * 128 + q * 32];
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)                // rows 64 p and 64 p + 32 of the block
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                mma_f16(acc[p][m][0], v[2 * p][0], v[2 * p + 1][0], v[2 * p][1], v[2 * p + 1][1],
+                                        x[m].x, x[m].y);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                mma_f16(acc[p][m][kChains - 1], v[2 * p][2], v[2 * p + 1][2], v[2 * p][3],
+                                        v[2 * p + 1][3], x[m].z, x[m].w);
                     }
                 }
+                __syncwarp();                      // every lane has read the slot
+                fetch();
+                if (++slot == pl.depth) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
             }
-            cluster_sync();                        // the peers' shared memory stays until it is read
         }
-        if (rank != 0 || slice != 0)
-            return;
+        if (kChains == 2)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    acc[p][0][0][v] += acc[p][0][kChains - 1][v];
+        // The tile's sums over its slices (value v by slice v mod slices), then
+        // to the block of the cluster that owns the round.
+        const int tile = tile_of(it);
+        if (pl.slices > 1) {
+            if (it > 0)
+                bar_group(1 + group, pl.slices);   // the previous round's sums are read
+#pragma unroll
+            for (int v = 0; v < kVals; ++v)
+                red[(slice * kVals + v) * 32] = acc[v / (4 * MT)][v / 4 % MT][0][v & 3];
+            bar_group(1 + group, pl.slices);
+        }
+        float *dst_own = sums + ((rank * pl.owned() + it / cluster) * pl.groups + group) * (kVals * 32) + lane;
+        uint32_t dst = 0;
+        if (cluster > 1) {
+            if (!peers_up) {
+                cluster_wait();                    // every block of the cluster has started
+                peers_up = true;
+            }
+            dst = map_shared_to_cta(smem_u32(dst_own), it % cluster);
+        }
+#pragma unroll
+        for (int v = 0; v < kVals; ++v) {
+            if (pl.slices > 1 && v % pl.slices != slice)
+                continue;
+            float s = acc[v / (4 * MT)][v / 4 % MT][0][v & 3];
+            if (pl.slices > 1) {
+                s = red[v * 32];
+                for (int k = 1; k < pl.slices; ++k)
+                    s += red[(k * kVals + v) * 32];
+            }
+            s = unscale(v, s);
+            if (cluster > 1)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 128 * v), "f"(s) : "memory");
+            else
+                store(tile, v, s);
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t n = row0 + 32 * j;
-        if (n >= a.N)
-            continue;
-        int seg = 0;
-        while (seg + 1 < a.nseg && n >= a.seg_end[seg])
-            ++seg;
-        const float gs = __ldg(a.gs + seg);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int row = 8 * m + 2 * t + c;
-                if (row < a.M)
-                    a.out[row * a.ldo + n] =
-                        __float2bfloat16_rn(__fdiv_rn(acc[j >> 1][m][2 * (j & 1) + c] * 256.0f, gs));
+    if (!ok && lane == 0)                          // copies still in flight have landed before the block ends
+        for (int d = 0; d < pl.depth; ++d)
+            mbar_wait(&bar[(slot + d) % pl.depth], slot + d < pl.depth ? phase : phase ^ 1u, &never_abort);
+    if (cluster > 1) {
+        if (!peers_up)
+            cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+        // the owned rounds: sums over the cluster's blocks in rank order
+        for (int it = rank; it < pl.rounds; it += cluster)
+            for (int v = slice; v < kVals; v += pl.slices) {
+                const float *p = sums + ((it / cluster) * pl.groups + group) * (kVals * 32) + v * 32 + lane;
+                float s = 0.0f;
+                for (int r = 0; r < cluster; ++r)
+                    s += p[r * pl.owned() * pl.groups * (kVals * 32)];
+                store(tile_of(it), v, s);
             }
     }
 }
 
-template <int MT>
-static cudaError_t launch_mt(const GemvArgs &a, int tiles, int slices, int cluster, cudaStream_t s)
+// The split (groups, slices, cluster) completed for a shape; panel 0: it does
+// not fit into shared memory.
+static GemvPlan complete_plan(const GemvArgs &a, int groups, int slices, int cluster, int num_sms)
 {
-    const int warps = tiles * slices;
+    constexpr int kMaxBytes = 225 * 1024;
+    const int mt = a.M <= 8 ? 1 : 2;
     const int64_t row_tiles = (a.N + 127) / 128 * 4;
+    const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
+    const int block_steps = (steps + cluster - 1) / cluster;
+    GemvPlan p{};
+    p.groups = groups;
+    p.slices = slices;
+    p.cluster = cluster;
+    const int64_t tiles = (row_tiles + groups - 1) / groups;
+    const int64_t rounds = (tiles + num_sms / cluster - 1) / (num_sms / cluster);
+    p.rounds = static_cast<int>(rounds);
+    p.clusters = static_cast<int>((tiles + rounds - 1) / rounds);
+    for (p.depth = kMaxDepth; p.depth > 2; --p.depth)      // the deepest ring beside the whole x
+        if (p.total(mt) + block_steps * mt * 4096 <= kMaxBytes)
+            break;
+    p.panel = std::min(block_steps, (kMaxBytes - p.total(mt)) / (4096 * mt));
+    return p;
+}
+
+template <int MT>
+static cudaError_t launch_mt(const GemvArgs &a, const GemvPlan &p, cudaStream_t s)
+{
+    static unsigned long long attr_done = 0;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(gemv_kernel<MT>), 226 * 1024, &attr_done);
+    if (e != cudaSuccess)
+        return e;
+    GemvMaps maps;
+    const uint64_t ld = static_cast<uint64_t>(a.K / 2);
+    if (code_map(&maps.rows, a.codes, a.N, a.K / 2, 8) != NVFP4_OK)
+        return cudaErrorInvalidValue;
+    maps.blocks = maps.rows;
+    if (a.N >= 128) {
+        const uint64_t dims[3] = {ld, 32, static_cast<uint64_t>(a.N / 32)}, strides[2] = {ld, 32 * ld};
+        const uint32_t box[3] = {128, 8, 4};
+        if (byte_map(&maps.blocks, a.codes, 3, dims, strides, box, true) != NVFP4_OK)
+            return cudaErrorInvalidValue;
+    }
+    {
+        const uint64_t dims[2] = {512, static_cast<uint64_t>((a.N + 127) / 128 * (a.K / 64))}, strides[1] = {512};
+        const uint32_t box[2] = {128, 4};
+        if (byte_map(&maps.scales, a.scales, 2, dims, strides, box, false) != NVFP4_OK)
+            return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((row_tiles + tiles - 1) / tiles * cluster));
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = warps > tiles || cluster > 1 ? sizeof(float) * 32 * 8 * MT * warps : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.clusters * p.cluster));
+    cfg.blockDim = dim3(32 * p.warps());
+    cfg.dynamicSmemBytes = p.total(MT) + 1024;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemv_kernel<MT>, a, slices, cluster);
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemv_kernel<MT>, maps, a, p);
 }
 
-cudaError_t launch_gemv_as(const GemvArgs &a, int tiles, int slices, int cluster, cudaStream_t s)
+cudaError_t launch_gemv_as(const GemvArgs &a, int groups, int slices, int cluster, int num_sms, cudaStream_t s)
 {
-    return a.M <= 8 ? launch_mt<1>(a, tiles, slices, cluster, s) : launch_mt<2>(a, tiles, slices, cluster, s);
+    const GemvPlan p = complete_plan(a, groups, slices, cluster, num_sms);
+    if (p.panel < 1)
+        return cudaErrorInvalidValue;
+    return a.M <= 8 ? launch_mt<1>(a, p, s) : launch_mt<2>(a, p, s);
 }
 
 cudaError_t launch_gemv(const GemvArgs &a, int num_sms, cudaStream_t s)
 {
     const int64_t row_tiles = (a.N + 127) / 128 * 4;
     const int64_t steps = (a.K + kStep - 1) / kStep;
-    int64_t parts = std::min<int64_t>(steps, 16LL * num_sms / row_tiles);
-    int cluster = 1, slices = 1, tiles = 4;
-    if (parts > 1) {
-        while (parts > 8 * cluster && cluster < 8)
-            cluster *= 2;
-        slices = static_cast<int>(std::min<int64_t>(8, (parts + cluster - 1) / cluster));
-        tiles = slices >= 3 ? 1 : 2;
-    }
-    return launch_gemv_as(a, tiles, slices, cluster, s);
+    int cluster = 1;
+    while (cluster < 8 && row_tiles * cluster * 2 <= num_sms && steps >= cluster * 2 * 4)
+        cluster *= 2;
+    const int slices = static_cast<int>(std::min<int64_t>(kMaxWarps, (steps + cluster - 1) / cluster));
+    int groups = kMaxWarps / slices;
+    while (groups > 1 && complete_plan(a, groups, slices, cluster, num_sms).panel < 1)
+        --groups;
+    return launch_gemv_as(a, groups, slices, cluster, num_sms, s);
 }
 
 } // namespace nvfp4

@@ -43,6 +43,15 @@ int moe_args_status(const nvfp4_moe_args *args, bool need_out);
 // not null), else the status to return (api.cu).
 int device_status(int *num_sms);
 
+// 2-D uint8 tensor map over row-major codes [rows, cols_bytes], boxes of
+// box_rows rows x 128 bytes with 128-byte swizzle (api.cu; after
+// device_status).
+int code_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols_bytes, int box_rows);
+// Tiled map over bytes of `rank` (2 or 3) dimensions, innermost first;
+// strides[i] is that of dimension i + 1; 128-byte or no swizzle.
+int byte_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+             const uint32_t *box, bool swizzle128);
+
 // Arguments of the persistent block-scaled FP4 GEMM engine (gemm.cu).
 struct GemmArgs {
     // scale factors, NVFP4_SCALES_MMA layout: one 128-row block = (K/64) atoms of 512 bytes
@@ -215,9 +224,9 @@ struct GemvArgs {
     int64_t ldo;
 };
 cudaError_t launch_gemv(const GemvArgs &args, int num_sms, cudaStream_t s);
-// The same with a given split: row tiles and k slices per block, blocks per
-// cluster (each of them a further split of k).
-cudaError_t launch_gemv_as(const GemvArgs &args, int tiles, int slices, int cluster, cudaStream_t s);
+// The same with a given split: row tiles and k slices at a time per block
+// (their product at most 16), blocks per cluster (each a further split of k).
+cudaError_t launch_gemv_as(const GemvArgs &args, int groups, int slices, int cluster, int num_sms, cudaStream_t s);
 
 // Router load statistics, balance loss and gradient (balance.cu).
 struct BalanceArgs {
