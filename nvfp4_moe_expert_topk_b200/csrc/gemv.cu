@@ -38,6 +38,7 @@
 // in shared memory in a fixed order.  Every wait on a copy is bounded: a warp
 // that gives up stops loading and ends with sums of what it has.
 #include <algorithm>
+#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -414,9 +415,36 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     acc[p][0][0][v] += acc[p][0][kChains - 1][v];
+        const int tile = tile_of(it);
+        if (pl.slices == 1 && cluster == 1) {
+            // nothing to add up: straight from the registers
+            const int64_t n0 = static_cast<int64_t>(tile >> 2) * 128 + (tile & 3) * 8 + g;
+            const bool one = a.nseg == 1 && n0 + 96 < a.N;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 8 * m + 2 * t + c;
+                    if (row < a.M) {
+                        if (one) {
+                            const float q = unscale(4 * m + c, 1.0f), inv = inv_gs[0];
+                            __nv_bfloat16 *o = a.out + row * a.ldo + n0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                o[32 * j] = __float2bfloat16_rn(acc[j >> 1][m][0][2 * (j & 1) + c] * q * inv);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int v = ((j >> 1) * MT + m) * 4 + 2 * (j & 1) + c;
+                                store(tile, v, unscale(v, acc[j >> 1][m][0][2 * (j & 1) + c]));
+                            }
+                        }
+                    }
+                }
+            continue;
+        }
         // The tile's sums over its slices (value v by slice v mod slices), then
         // to the block of the cluster that owns the round.
-        const int tile = tile_of(it);
         if (pl.slices > 1) {
             if (it > 0)
                 bar_group(1 + group, pl.slices);   // the previous round's sums are read
@@ -471,35 +499,94 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     }
 }
 
-// The split (groups, slices, cluster) completed for a shape; panel 0: it does
-// not fit into shared memory.
-static GemvPlan complete_plan(const GemvArgs &a, int groups, int slices, int cluster, int num_sms)
+constexpr int kMaxBytes = 225 * 1024;              // dynamic shared memory of a block
+
+// Clusters of `cluster` blocks (a power of two up to 8) that fit on the current
+// device at once, one block per SM; asked once per device and size.  A cluster
+// lies in one group of SMs, so fewer fit than SMs / cluster.
+int gemv_clusters(int cluster, int num_sms)
 {
-    constexpr int kMaxBytes = 225 * 1024;
+    constexpr int kMaxDev = 64;
+    static int cached[kMaxDev][4];                 // 0: not yet asked
+    static std::mutex mu;
+    if (cluster == 1)
+        return num_sms;
+    const int size = cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)
+        return num_sms / cluster;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev][size] > 0)
+        return cached[dev][size];
+    int n = 0;
+    if (cudaFuncSetAttribute(gemv_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBytes + 1024) ==
+        cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms / cluster * cluster));
+        cfg.blockDim = dim3(32 * kMaxWarps);
+        cfg.dynamicSmemBytes = kMaxBytes + 1024;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, gemv_kernel<2>, &cfg) != cudaSuccess)
+            n = 0;
+    }
+    (void)cudaGetLastError();
+    if (n <= 0 || n > num_sms / cluster)
+        n = num_sms / cluster;
+    cached[dev][size] = n;
+    return n;
+}
+
+// The split (groups, slices, cluster) completed for a shape, `fit` clusters at
+// a time; panel < 1: it does not fit into shared memory.
+static GemvPlan complete_plan(const GemvArgs &a, int groups, int slices, int cluster, int fit)
+{
     const int mt = a.M <= 8 ? 1 : 2;
-    const int64_t row_tiles = (a.N + 127) / 128 * 4;
+    const int row_tiles = static_cast<int>((a.N + 127) / 128 * 4);
     const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
     const int block_steps = (steps + cluster - 1) / cluster;
     GemvPlan p{};
     p.groups = groups;
     p.slices = slices;
     p.cluster = cluster;
-    const int64_t tiles = (row_tiles + groups - 1) / groups;
-    const int64_t rounds = (tiles + num_sms / cluster - 1) / (num_sms / cluster);
-    p.rounds = static_cast<int>(rounds);
-    p.clusters = static_cast<int>((tiles + rounds - 1) / rounds);
-    for (p.depth = kMaxDepth; p.depth > 2; --p.depth)      // the deepest ring beside the whole x
-        if (p.total(mt) + block_steps * mt * 4096 <= kMaxBytes)
-            break;
+    const int tiles = (row_tiles + groups - 1) / groups;
+    p.rounds = (tiles + fit - 1) / fit;
+    p.clusters = (tiles + p.rounds - 1) / p.rounds;
+    p.depth = 2;                                           // deeper beside the whole x where there is room
+    const int room = kMaxBytes - p.total(mt);
+    p.depth += std::min(kMaxDepth - 2, std::max(0, (room - block_steps * mt * 4096) / (p.ring() / 2)));
     p.panel = std::min(block_steps, (kMaxBytes - p.total(mt)) / (4096 * mt));
     return p;
+}
+
+// Estimated time of a plan in 10 ns.  The weights of the terms are a fit to the
+// device times of all splits of 20 shapes (M 1 to 16, N 33 to 65536, K 64 to
+// 16384; off by 10 % rms, and the split it picks within 3 % of the best one
+// tried for most of them, 15 % at worst): a round's steps cost a latency and a
+// share per warp (decoding is bound by issue slots), plus the meeting of the
+// slices, the block's pieces of x per warp, and the meeting of the cluster.
+static int plan_cost(const GemvPlan &p, int mt, int steps)
+{
+    const int block_steps = (steps + p.cluster - 1) / p.cluster;
+    const int s = (block_steps + p.slices - 1) / p.slices, w = p.warps();
+    const int pieces = (block_steps * 8 + w - 1) / w;
+    const bool sl = p.slices > 1, cl = p.cluster > 1;
+    if (p.panel < block_steps)                             // x converted again for every tile
+        return (1 << 28) + p.rounds * block_steps;
+    return mt == 1 ? p.rounds * (s * (58 + 10 * w) + 41 * sl + 56 * cl + 58) + 20 * pieces + 145 * cl
+                   : p.rounds * (s * (79 + 14 * w) + 163 * sl + 219 * cl + 12) + 48 * pieces + 181 * cl;
 }
 
 template <int MT>
 static cudaError_t launch_mt(const GemvArgs &a, const GemvPlan &p, cudaStream_t s)
 {
     static unsigned long long attr_done = 0;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(gemv_kernel<MT>), 226 * 1024, &attr_done);
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(gemv_kernel<MT>), kMaxBytes + 1024, &attr_done);
     if (e != cudaSuccess)
         return e;
     GemvMaps maps;
@@ -536,9 +623,8 @@ static cudaError_t launch_mt(const GemvArgs &a, const GemvPlan &p, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, gemv_kernel<MT>, maps, a, p);
 }
 
-cudaError_t launch_gemv_as(const GemvArgs &a, int groups, int slices, int cluster, int num_sms, cudaStream_t s)
+static cudaError_t launch_plan(const GemvArgs &a, const GemvPlan &p, cudaStream_t s)
 {
-    const GemvPlan p = complete_plan(a, groups, slices, cluster, num_sms);
     if (p.panel < 1)
         return cudaErrorInvalidValue;
     return a.M <= 8 ? launch_mt<1>(a, p, s) : launch_mt<2>(a, p, s);
@@ -546,16 +632,22 @@ cudaError_t launch_gemv_as(const GemvArgs &a, int groups, int slices, int cluste
 
 cudaError_t launch_gemv(const GemvArgs &a, int num_sms, cudaStream_t s)
 {
-    const int64_t row_tiles = (a.N + 127) / 128 * 4;
-    const int64_t steps = (a.K + kStep - 1) / kStep;
-    int cluster = 1;
-    while (cluster < 8 && row_tiles * cluster * 2 <= num_sms && steps >= cluster * 2 * 4)
-        cluster *= 2;
-    const int slices = static_cast<int>(std::min<int64_t>(kMaxWarps, (steps + cluster - 1) / cluster));
-    int groups = kMaxWarps / slices;
-    while (groups > 1 && complete_plan(a, groups, slices, cluster, num_sms).panel < 1)
-        --groups;
-    return launch_gemv_as(a, groups, slices, cluster, num_sms, s);
+    const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
+    GemvPlan best{};
+    int least = 0;
+    for (int cluster = 1; cluster <= 8 && cluster <= steps; cluster *= 2) {
+        const int fit = gemv_clusters(cluster, num_sms);
+        for (int groups = 1; groups <= kMaxWarps; ++groups)
+            for (int slices = 1; slices * groups <= kMaxWarps && slices * cluster <= steps; ++slices) {
+                const GemvPlan p = complete_plan(a, groups, slices, cluster, fit);
+                const int cost = p.panel < 1 ? 1 << 30 : plan_cost(p, a.M <= 8 ? 1 : 2, steps);
+                if (best.groups == 0 || cost < least) {
+                    best = p;
+                    least = cost;
+                }
+            }
+    }
+    return launch_plan(a, best, s);
 }
 
 } // namespace nvfp4

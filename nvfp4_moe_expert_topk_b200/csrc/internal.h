@@ -224,10 +224,6 @@ struct GemvArgs {
     int64_t ldo;
 };
 cudaError_t launch_gemv(const GemvArgs &args, int num_sms, cudaStream_t s);
-// The same with a given split: row tiles and k slices at a time per block
-// (their product at most 16), blocks per cluster (each a further split of k).
-cudaError_t launch_gemv_as(const GemvArgs &args, int groups, int slices, int cluster, int num_sms, cudaStream_t s);
-
 // Router load statistics, balance loss and gradient (balance.cu).
 struct BalanceArgs {
     const float *logits;

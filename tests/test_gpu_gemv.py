@@ -131,6 +131,12 @@ def test_random_shapes(seed):
     check(M, N, K, seed=seed, seg=cuts, ldx=8 * int(rng.integers(0, 3)), ldo=int(rng.integers(0, 5)))
 
 
+@pytest.mark.parametrize("M", [2, 16])
+def test_long_k(M):
+    """More columns than the block holds of x at a time."""
+    check(M, 70, 131072 + 64, seed=1)
+
+
 def test_extreme_values():
     """Activations over the whole bf16 range; zero rows; a row that is not
     finite spoils only itself."""
