@@ -355,48 +355,55 @@ def nvfp4_debug_bounded_wait(flag, target, err, stream=None):
 
 # ---- operators around the routed block.  Single-token calls of these take a
 # few microseconds on the device, so their marshalling is kept short: pointers
-# travel as plain integers, every tensor's device is compared once, and the
-# launch goes to the device of the tensors (which need not be the current one).
-def _on(dev, t, name, dtype):
-    """Data pointer of a contiguous tensor on CUDA device `dev`."""
+# travel as plain integers, the checks that pass cost one comparison each, and
+# the message is worked out only for the one that fails.  The launch goes to
+# the device of the tensors (which need not be the current one).
+_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_Tensor = torch.Tensor
+
+
+def _refuse(dev, t, name, dtype, shape=None):
+    """Raises the ValueError that says what is wrong with `t`."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required" if t is None else f"{name} must be a CUDA tensor")
+    if dev is None or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" + ("" if dev is None else f" on cuda:{dev}, got {t.device}"))
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if shape is not None:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _on(dev, t, name, dtype):
+    """Data pointer of a contiguous tensor on CUDA device `dev`."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(dev, t, name, dtype)
 
 
 def _rows_on(dev, t, name, shape):
     """(data pointer, row stride) of a bf16 matrix whose rows may be strided."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} is required" if t is None else f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    if shape[0] <= 1 or shape[1] == 0:
-        ld = max(ld, (shape[1] + 7) // 8 * 8)      # the stride of a single row is not used
-        ld += -ld % 8
-    return t.data_ptr(), ld
+    if isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        ld, step = t.stride()
+        if step == 1 or shape[1] == 1:
+            return t.data_ptr(), ld
+    _refuse(dev, t, name, _BF16, shape)
 
 
 def _first(t, name):
     """The CUDA device index the call runs on: that of its first tensor."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise ValueError(f"{name} must be a CUDA tensor" if t is not None else f"{name} is required")
-    return t.get_device()
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        return t.get_device()
+    _refuse(None, t, name, None)
 
 
-def _elements(t, name, n):
+def _holds(t, name, n):
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
 
@@ -405,12 +412,12 @@ def _run(dev, stream, where, call, *args):
     """call(*args, stream) with `dev` current, on `stream` or the device's
     current stream."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = _raw_stream(dev)
     else:
         if stream.device_index != dev:
             raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
         raw = stream.cuda_stream
-    if dev == torch._C._cuda_getDevice():
+    if dev == _current_device():
         st = call(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -433,38 +440,36 @@ def nvfp4_add_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, 
     if len(shape) != 2:
         raise ValueError(f"x must be [T, H], got {list(shape)}")
     T, H = shape
-    a = NormArgs()
-    a.T, a.H, a.eps, a.quant, a.scale_layout = T, H, eps, quant, scale_layout
-    a.x, a.ldx = _rows_on(dev, x, "x", shape)
-    a.weight = _on(dev, weight, "weight", torch.bfloat16)
-    _elements(weight, "weight", H)
-    if (residual is None) != (residual_out is None):
+    px, ldx = _rows_on(dev, x, "x", shape)
+    pw = _on(dev, weight, "weight", _BF16)
+    _holds(weight, "weight", H)
+    pr = po = py = pg = pc = ps = None
+    ldr = ldo = ldy = 0
+    if residual is not None and residual_out is not None:
+        pr, ldr = _rows_on(dev, residual, "residual", shape)
+        po, ldo = _rows_on(dev, residual_out, "residual_out", shape)
+    elif residual is not residual_out:
         raise ValueError("residual and residual_out come together")
-    if residual is not None:
-        a.residual, a.ldr = _rows_on(dev, residual, "residual", shape)
-        a.residual_out, a.ldro = _rows_on(dev, residual_out, "residual_out", shape)
     if y is not None:
-        a.y, a.ldy = _rows_on(dev, y, "y", shape)
+        py, ldy = _rows_on(dev, y, "y", shape)
     elif quant == NVFP4_QUANT_NONE:
         raise ValueError("y is required without a quantised output")
     if quant == NVFP4_QUANT_NVFP4:
-        a.gs = _on(dev, gs, "gs", torch.float32)
-        a.codes = _on(dev, codes, "codes", torch.uint8)
-        a.scales = _on(dev, scales, "scales", torch.uint8)
-        _elements(gs, "gs", 1)
-        _elements(codes, "codes", T * (H // 2))
-        need = nvfp4_scales_bytes(T, H, scale_layout)
+        pg = _on(dev, gs, "gs", _F32)
+        pc = _on(dev, codes, "codes", _U8)
+        ps = _on(dev, scales, "scales", _U8)
+        _holds(gs, "gs", 1)
+        _holds(codes, "codes", T * (H // 2))
+        need = (T if scale_layout == NVFP4_SCALES_ROWMAJOR else T + 127 & -128) * (H // 16)
         if scales.numel() < need:
             raise ValueError(f"scales must hold {need} bytes, got {scales.numel()}")
     elif quant == NVFP4_QUANT_E4M3:
-        if codes is not None and codes.dtype == torch.float8_e4m3fn:
-            a.codes = _on(dev, codes, "codes", torch.float8_e4m3fn)
-        else:
-            a.codes = _on(dev, codes, "codes", torch.uint8)
-        a.scales = _on(dev, scales, "scales", torch.float32)
-        _elements(codes, "codes", T * H)
-        _elements(scales, "scales", T * ((H + 127) // 128))
-    _run(dev, stream, "nvfp4_add_rmsnorm", lib().nvfp4_add_rmsnorm, a)
+        pc = _on(dev, codes, "codes", _F8 if codes is not None and codes.dtype is _F8 else _U8)
+        ps = _on(dev, scales, "scales", _F32)
+        _holds(codes, "codes", T * H)
+        _holds(scales, "scales", T * ((H + 127) // 128))
+    _run(dev, stream, "nvfp4_add_rmsnorm", lib().nvfp4_add_rmsnorm,
+         NormArgs(px, pr, pw, T, H, ldx, ldr, ldo, ldy, eps, po, py, quant, scale_layout, pg, pc, ps))
 
 
 def nvfp4_gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
@@ -472,19 +477,21 @@ def nvfp4_gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
     in NVFP4 (scales in the MMA layout, b_gs one global scale per segment of
     rows ending at seg_end); rows of x and out may be strided."""
     dev = _first(x, "x")
-    M, K = x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [M, K], got {list(shape)}")
+    M, K = shape
+    pc = _on(dev, b_codes, "b_codes", _U8)
     N = b_codes.shape[0]
-    px, ldx = _rows_on(dev, x, "x", x.shape)
+    px, ldx = _rows_on(dev, x, "x", shape)
     po, ldo = _rows_on(dev, out, "out", (M, N))
-    pc = _on(dev, b_codes, "b_codes", torch.uint8)
-    _elements(b_codes, "b_codes", N * (K // 2))
-    ps = _on(dev, b_scales, "b_scales", torch.uint8)
-    if b_scales.numel() < (N + 127) // 128 * 128 * (K // 16):
-        raise ValueError(f"b_scales must hold {nvfp4_scales_bytes(N, K, NVFP4_SCALES_MMA)} bytes, "
-                         f"got {b_scales.numel()}")
-    pg = _on(dev, b_gs, "b_gs", torch.float32)
+    _holds(b_codes, "b_codes", N * (K // 2))
+    ps = _on(dev, b_scales, "b_scales", _U8)
+    if b_scales.numel() < (N + 127 & -128) * (K // 16):
+        raise ValueError(f"b_scales must hold {(N + 127 & -128) * (K // 16)} bytes, got {b_scales.numel()}")
+    pg = _on(dev, b_gs, "b_gs", _F32)
     nseg = len(seg_end)
-    _elements(b_gs, "b_gs", nseg)
+    _holds(b_gs, "b_gs", nseg)
     _run(dev, stream, "nvfp4_gemv", lib().nvfp4_gemv, px, M, ldx, pc, ps, pg, (ctypes.c_int64 * nseg)(*seg_end), nseg,
          N, K, po, ldo)
 
@@ -495,14 +502,16 @@ def nvfp4_moe_balance_workspace_size(T, S, E):
 
 def _balance_inputs(logits, topk_ids, k, seq_offsets):
     dev = _first(logits, "logits")
+    pl = _on(dev, logits, "logits", _F32)
+    pi = _on(dev, topk_ids, "topk_ids", _I32)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {list(logits.shape)}")
     T, E = logits.shape
-    pl = _on(dev, logits, "logits", torch.float32)
-    pi = _on(dev, topk_ids, "topk_ids", torch.int32)
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_ids.shape[1] < k:
         raise ValueError(f"topk_ids must be [{T}, >= {k}], got {list(topk_ids.shape)}")
     if seq_offsets is None:
         return dev, pl, pi, topk_ids.shape[1], T, E, None, 1
-    po = _on(dev, seq_offsets, "seq_offsets", torch.int32)
+    po = _on(dev, seq_offsets, "seq_offsets", _I32)
     return dev, pl, pi, topk_ids.shape[1], T, E, po, seq_offsets.numel() - 1
 
 
@@ -514,13 +523,13 @@ def nvfp4_moe_balance(logits, topk_ids, k, counts, tokens, probs, loss, workspac
     [S] fp32; seq_offsets int32 [S + 1] (None: one sequence); workspace: uint8,
     nvfp4_moe_balance_workspace_size(T, S, E) bytes."""
     dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
-    pc, pt = _on(dev, counts, "counts", torch.int32), _on(dev, tokens, "tokens", torch.int32)
-    pp, ps = _on(dev, probs, "probs", torch.float32), _on(dev, loss, "loss", torch.float32)
-    pw = _on(dev, workspace, "workspace", torch.uint8)
-    _elements(counts, "counts", S * E)
-    _elements(tokens, "tokens", S)
-    _elements(probs, "probs", S * E)
-    _elements(loss, "loss", S)
+    pc, pt = _on(dev, counts, "counts", _I32), _on(dev, tokens, "tokens", _I32)
+    pp, ps = _on(dev, probs, "probs", _F32), _on(dev, loss, "loss", _F32)
+    pw = _on(dev, workspace, "workspace", _U8)
+    _holds(counts, "counts", S * E)
+    _holds(tokens, "tokens", S)
+    _holds(probs, "probs", S * E)
+    _holds(loss, "loss", S)
     _run(dev, stream, "nvfp4_moe_balance", lib().nvfp4_moe_balance, pl, pi, ld, T, E, k, po, S, scoring, pc, pt, pp,
          ps, pw, workspace.numel())
 
@@ -531,15 +540,15 @@ def nvfp4_moe_balance_backward(logits, topk_ids, k, counts, tokens, grad_loss, g
     of sum grad_weights * topk_weights when grad_weights [T, k] is given) with
     respect to the logits; counts and tokens as nvfp4_moe_balance wrote them."""
     dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
-    pc, pt = _on(dev, counts, "counts", torch.int32), _on(dev, tokens, "tokens", torch.int32)
-    pg, pd = _on(dev, grad_loss, "grad_loss", torch.float32), _on(dev, grad_logits, "grad_logits", torch.float32)
-    _elements(counts, "counts", S * E)
-    _elements(tokens, "tokens", S)
-    _elements(grad_loss, "grad_loss", S)
-    _elements(grad_logits, "grad_logits", T * E)
+    pc, pt = _on(dev, counts, "counts", _I32), _on(dev, tokens, "tokens", _I32)
+    pg, pd = _on(dev, grad_loss, "grad_loss", _F32), _on(dev, grad_logits, "grad_logits", _F32)
+    _holds(counts, "counts", S * E)
+    _holds(tokens, "tokens", S)
+    _holds(grad_loss, "grad_loss", S)
+    _holds(grad_logits, "grad_logits", T * E)
     pw = None
     if grad_weights is not None:
-        pw = _on(dev, grad_weights, "grad_weights", torch.float32)
-        _elements(grad_weights, "grad_weights", T * k)
+        pw = _on(dev, grad_weights, "grad_weights", _F32)
+        _holds(grad_weights, "grad_weights", T * k)
     _run(dev, stream, "nvfp4_moe_balance_backward", lib().nvfp4_moe_balance_backward, pl, pi, ld, T, E, k, po, S,
          scoring, pc, pt, pg, pw, pd)
