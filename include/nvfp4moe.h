@@ -428,7 +428,7 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
  * (the first k of each row; ld_ids > k: e.g. the rows of
  * nvfp4_moe_topk_shared, whose shared slots are not counted).  An id outside
  * [0, E) is a skipped slot; a token whose k slots are all skipped is padding:
- * its logits are not read and it counts nowhere.  seq_offsets: device int32
+ * it counts nowhere, whatever its logits hold.  seq_offsets: device int32
  * [S + 1], non-decreasing in [0, T]; sequence s is the tokens
  * [seq_offsets[s], seq_offsets[s+1]), tokens outside every sequence are
  * ignored; NULL: one sequence of all T tokens (S = 1).  With p = softmax(l)
@@ -444,8 +444,8 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
  * over the chunks, in a fixed order.  The workspace (caller-owned,
  * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
  * scratch: calls sharing one must not overlap on the device.
- * 1 <= k <= min(E, 32), E <= 1024, S >= 1, T >= 0 (T = 0: logits and topk_ids
- * may be NULL; zeros are written).  Two launches. */
+ * 1 <= k <= min(E, 32), E <= 1024, 1 <= S <= 65535, T >= 0 (T = 0: logits and
+ * topk_ids may be NULL; zeros are written).  Two launches. */
 size_t nvfp4_moe_balance_workspace_size(int64_t T, int64_t S, int E);
 int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_ids, int64_t T, int E, int k,
                       const int32_t *seq_offsets, int64_t S, int scoring,

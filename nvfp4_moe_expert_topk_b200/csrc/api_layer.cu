@@ -18,19 +18,22 @@ int status_of(cudaError_t e)
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-// Workspace of nvfp4_moe_balance: per chunk slot E probability sums, E counts
-// and the token count.
+// Workspace of nvfp4_moe_balance: per chunk slot E probability sums and E
+// counts (padded to 4) and the token count; per sequence the loss's parts and
+// a counter.
 struct BalanceLayout {
-    int64_t slots, part_c, part_n, total;
+    int64_t part_c, part_dot, part_n, done, total;
 };
 
 BalanceLayout balance_layout(int64_t T, int64_t S, int64_t E)
 {
     BalanceLayout L;
-    L.slots = balance_slots(T, S);
-    L.part_c = L.slots * E * 4;
-    L.part_n = 2 * L.part_c;
-    L.total = L.part_n + 4 * L.slots;
+    const int64_t slots = balance_slots(T, S, static_cast<int>(E)), row = (E + 3) / 4 * 16;
+    L.part_c = slots * row;
+    L.part_dot = 2 * L.part_c;
+    L.part_n = L.part_dot + S * balance_sum_blocks(static_cast<int>(E)) * 8;
+    L.done = L.part_n + 4 * slots;
+    L.total = L.done + 4 * S;
     return L;
 }
 
@@ -40,7 +43,7 @@ int check_balance(int64_t T, int64_t S, int E, int k, int64_t ld_ids, int scorin
         return NVFP4_ERR_INVALID_ARG;
     if (scoring != NVFP4_SCORING_SOFTMAX && scoring != NVFP4_SCORING_SIGMOID)
         return NVFP4_ERR_INVALID_ARG;
-    if (E > 1024 || k > 32 || k > E || T >= (1LL << 31) - 1024 || S > (1LL << 24))
+    if (E > 1024 || k > 32 || k > E || T >= (1LL << 31) - 1024 || S > 65535)
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
     return NVFP4_OK;
 }
@@ -194,7 +197,7 @@ int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_i
     a.S = static_cast<int>(S);
     a.offsets = seq_offsets;
     a.scoring = scoring;
-    a.chunk = balance_chunk(T);
+    a.chunk = balance_chunk(T, E);
     a.counts = counts;
     a.tokens = tokens;
     a.probs = probs;
@@ -202,6 +205,8 @@ int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_i
     a.part_p = reinterpret_cast<float *>(ws);
     a.part_c = reinterpret_cast<int32_t *>(ws + L.part_c);
     a.part_n = reinterpret_cast<int32_t *>(ws + L.part_n);
+    a.part_dot = reinterpret_cast<double *>(ws + L.part_dot);
+    a.done = reinterpret_cast<int32_t *>(ws + L.done);
     return status_of(launch_balance(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -18,6 +18,12 @@
 // search, and a ragged batch needs no host-side plan.  Every chunk leaves its
 // sums in the workspace and a second kernel adds them in slot order: no
 // floating-point atomics, so results do not depend on timing.
+//
+// Both directions stream the logits once (4 bytes read per logit, 4 written
+// by the gradient) and are bound by HBM on long batches and by latency on
+// short ones: one warp per token with the row in registers, and the next
+// token's row, ids and weight gradients are loaded while the current one is
+// worked on.
 #include "internal.h"
 #include "quant.cuh"
 
@@ -27,7 +33,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kWholeThreads = 512;          // block of the one-launch form for short batches
+constexpr int kWholeTokens = 512;           // the longest batch it takes
 constexpr unsigned kAll = 0xffffffffu;
+
+// Columns of a chunk's row of sums, so that rows start on 16 bytes.
+__host__ __device__ constexpr int padded(int E) { return (E + 3) & ~3; }
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -43,6 +54,28 @@ __device__ __forceinline__ float warp_max(float v)
     for (int o = 16; o > 0; o >>= 1)
         v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
     return v;
+}
+
+// exp(x), x <= 0 or moderate: 2^(x log2 e) on the special-function unit, off by
+// 2 ulp and by the rounding of the product (|x| 2^-24 relative).
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+// 1 / x within 1 ulp; 0 for infinity.
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float sigmoid_fast(float x)
+{
+    return rcp_fast(1.0f + exp_fast(-x));
 }
 
 // Start of sequence s (s = S: end of the last), clamped into [0, T].
@@ -109,13 +142,13 @@ struct Row {
                 m = 0.0f;
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q) {
-                v[q] = expf(v[q] - m);
+                v[q] = exp_fast(v[q] - m);
                 sum += v[q];
             }
         } else {
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q) {
-                v[q] = __frcp_rn(1.0f + expf(-v[q]));
+                v[q] = sigmoid_fast(v[q]);
                 sum += v[q];
             }
         }
@@ -126,31 +159,67 @@ struct Row {
 
 } // namespace
 
-// Sums of one chunk slot: counts, tokens and probabilities.
-template <int P, bool V4>
-__global__ void __launch_bounds__(kThreads) balance_chunk_kernel(const BalanceArgs a)
+// Slot lane's id as stored (read ahead: checked when it is used).
+__device__ __forceinline__ int raw_id(const BalanceArgs &a, int t, int lane)
 {
-    extern __shared__ float sm[];                 // [kWarps][E] probability sums, then [E] int counts
+    return lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
+}
+
+// Tokens a warp has on their way: short rows need several to fill the memory's
+// latency, a long row is enough by itself.
+__host__ __device__ constexpr int tokens_ahead(int P) { return P == 1 ? 4 : P == 2 ? 2 : 1; }
+
+// Blocks per SM, by the registers that a row of up to 128 P columns takes.
+__host__ __device__ constexpr int chunk_blocks(int P) { return P <= 3 ? 4 : P <= 4 ? 3 : 2; }
+__host__ __device__ constexpr int backward_blocks(int P) { return P <= 3 ? 3 : 2; }
+
+// Sums of a run of tokens of one sequence: a chunk's, left in the workspace, or
+// (WHOLE, short batches) a whole sequence's, with its loss, in one launch.
+template <int P, bool V4, bool WHOLE>
+__global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : chunk_blocks(P)) balance_chunk_kernel(const BalanceArgs a)
+{
+    constexpr int W = (WHOLE ? kWholeThreads : kThreads) / 32, D = tokens_ahead(P);
+    extern __shared__ float sm[];                 // [W][E] probability sums, then [E] int counts
     __shared__ int tokens_s;
+    __shared__ double red[W];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, slot = blockIdx.x;
-    // the last sequence whose first slot is <= slot
-    int lo = 0, hi = a.S;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first_slot(a, mid) <= slot)
-            lo = mid;
-        else
-            hi = mid;
+    int seq, t0, t1;
+    if (WHOLE) {
+        seq = slot;
+        t0 = seq_start(a, seq);
+        t1 = seq_start(a, seq + 1);
+    } else {
+        // the last sequence whose first slot is <= slot
+        int lo = 0, hi = a.S;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first_slot(a, mid) <= slot)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        seq = lo;
+        slot_tokens(a, seq, slot, t0, t1);
+        if (t0 >= t1)
+            return;
     }
-    int t0, t1;
-    slot_tokens(a, lo, slot, t0, t1);
-    if (t0 >= t1)
-        return;
-    int *hist = reinterpret_cast<int *>(sm + kWarps * E);
-    for (int e = threadIdx.x; e < E; e += kThreads)
+    // (a padded token's logits are not used, but they are there to be read)
+    Row<P, V4> ring[D];
+    int ids[D];
+    auto fetch = [&](int u, int t) {
+        if (t < t1) {
+            ids[u] = raw_id(a, t, lane);
+            ring[u].load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        fetch(u, t0 + warp + u * W);
+    int *hist = reinterpret_cast<int *>(sm + W * E);
+    for (int e = threadIdx.x; e < E; e += 32 * W)
         hist[e] = 0;
     if (threadIdx.x == 0)
         tokens_s = 0;
@@ -160,20 +229,26 @@ __global__ void __launch_bounds__(kThreads) balance_chunk_kernel(const BalanceAr
     for (int q = 0; q < 4 * P; ++q)
         acc[q] = 0.0f;
     int tokens = 0;
-    for (int t = t0 + warp; t < t1; t += kWarps) {
-        const int id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
-        const bool on = id >= 0 && id < E;
-        if (!__any_sync(kAll, on))
-            continue;                              // a padded token
-        ++tokens;
-        if (on)
-            atomicAdd(hist + id, 1);
-        Row<P, V4> r;
-        r.load(a.logits + static_cast<int64_t>(t) * E, E, lane);
-        const float inv = r.scores(a.scoring);
+    for (int tb = t0 + warp; tb < t1; tb += D * W) {
 #pragma unroll
-        for (int q = 0; q < 4 * P; ++q)
-            acc[q] = fmaf(r.v[q], inv, acc[q]);
+        for (int u = 0; u < D; ++u) {
+            const int t = tb + u * W;
+            if (t >= t1)
+                break;
+            Row<P, V4> r = ring[u];
+            const int id = ids[u];
+            const bool on = id >= 0 && id < E;
+            fetch(u, t + D * W);
+            if (!__any_sync(kAll, on))
+                continue;                          // a padded token
+            ++tokens;
+            if (on)
+                atomicAdd(hist + id, 1);
+            const float inv = r.scores(a.scoring);
+#pragma unroll
+            for (int q = 0; q < 4 * P; ++q)
+                acc[q] = fmaf(r.v[q], inv, acc[q]);
+        }
     }
     if (lane == 0 && tokens)
         atomicAdd(&tokens_s, tokens);
@@ -184,63 +259,140 @@ __global__ void __launch_bounds__(kThreads) balance_chunk_kernel(const BalanceAr
             sm[warp * E + c] = acc[q];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {
+    const int Ep = padded(E);
+    double dot = 0.0;
+    for (int e = threadIdx.x; e < E; e += 32 * W) {
         float p = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < W; ++w)
             p += sm[w * E + e];
-        a.part_p[static_cast<int64_t>(slot) * E + e] = p;
-        a.part_c[static_cast<int64_t>(slot) * E + e] = hist[e];
+        if (WHOLE) {
+            a.counts[static_cast<int64_t>(seq) * E + e] = hist[e];
+            a.probs[static_cast<int64_t>(seq) * E + e] = p;
+            dot += static_cast<double>(hist[e]) * p;
+        } else {
+            a.part_p[static_cast<int64_t>(slot) * Ep + e] = p;
+            a.part_c[static_cast<int64_t>(slot) * Ep + e] = hist[e];
+        }
     }
-    if (threadIdx.x == 0)
+    if (WHOLE) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            dot += __shfl_xor_sync(kAll, dot, o);
+        if (lane == 0)
+            red[warp] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < W; ++w)
+                dot += red[w];
+            const double n = tokens_s;
+            a.tokens[seq] = tokens_s;
+            a.loss[seq] = tokens_s == 0 ? 0.0f : static_cast<float>(dot * E / (a.k * n * n));
+        }
+    } else if (threadIdx.x == 0) {
         a.part_n[slot] = tokens_s;
+        if (slot == first_slot(a, seq))
+            a.done[seq] = 0;                       // the second kernel's blocks of this sequence count themselves
+    }
 }
 
-// One block per sequence: its chunks' sums in slot order, and the loss.
+// Sums over a sequence's chunks: block (x, s) does kCols experts of sequence s,
+// thread (c, i) four of them in the chunks i, i + kRows, ...; the sums of the
+// kRows threads are added in order.  The loss is the sum of the blocks' parts
+// in block order, by the block that finds all others done.
+constexpr int kCols = 32, kRows = kThreads / (kCols / 4);
+
 __global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalanceArgs a)
 {
-    __shared__ double red[kWarps];
+    __shared__ double sp[kRows][kCols + 1];
+    __shared__ int sc[kRows][kCols + 1];
+    __shared__ int sn[kThreads / 32];
+    __shared__ int last_s;
     pdl_wait();
     pdl_trigger();
-    const int s = blockIdx.x, E = a.E;
+    const int s = blockIdx.y, E = a.E, Ep = padded(E);
     const int o0 = seq_start(a, s), o1 = seq_start(a, s + 1);
     const int slot0 = first_slot(a, s);
     const int nslots = o1 > o0 ? (o1 - 1) / a.chunk - o0 / a.chunk + 1 : 0;    // non-empty ones
-    int n = 0;
-    for (int i = 0; i < nslots; ++i)
-        n += a.part_n[slot0 + i];
-    double dot = 0.0;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-        double p = 0.0;
-        int c = 0;
-        for (int i = 0; i < nslots; ++i) {
-            p += a.part_p[static_cast<int64_t>(slot0 + i) * E + e];
-            c += a.part_c[static_cast<int64_t>(slot0 + i) * E + e];
+    const int c4 = 4 * (threadIdx.x % (kCols / 4)), row = threadIdx.x / (kCols / 4);
+    const int e0 = blockIdx.x * kCols + c4;
+    double p[4] = {0.0, 0.0, 0.0, 0.0};
+    int c[4] = {0, 0, 0, 0};
+    if (e0 < E) {
+        const float *pp = a.part_p + static_cast<int64_t>(slot0) * Ep + e0;
+        const int32_t *pc = a.part_c + static_cast<int64_t>(slot0) * Ep + e0;
+#pragma unroll 4
+        for (int i = row; i < nslots; i += kRows) {
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(pp + static_cast<int64_t>(i) * Ep));
+            const int4 n = __ldcg(reinterpret_cast<const int4 *>(pc + static_cast<int64_t>(i) * Ep));
+            p[0] += f.x, p[1] += f.y, p[2] += f.z, p[3] += f.w;
+            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
         }
-        a.counts[static_cast<int64_t>(s) * E + e] = c;
-        a.probs[static_cast<int64_t>(s) * E + e] = static_cast<float>(p);
-        dot += c * p;
+    }
+    int n = 0;
+    for (int i = threadIdx.x; i < nslots; i += kThreads)
+        n += __ldcg(a.part_n + slot0 + i);
+    n = __reduce_add_sync(kAll, n);
+    if ((threadIdx.x & 31) == 0)
+        sn[threadIdx.x >> 5] = n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        sp[row][c4 + j] = p[j];
+        sc[row][c4 + j] = c[j];
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32)
+        return;
+    n = 0;
+    for (int w = 0; w < kThreads / 32; ++w)
+        n += sn[w];
+    const int e = blockIdx.x * kCols + threadIdx.x;
+    double dot = 0.0;
+    if (e < E) {
+        double ps = 0.0;
+        int cs = 0;
+#pragma unroll 8
+        for (int i = 0; i < kRows; ++i) {
+            ps += sp[i][threadIdx.x];
+            cs += sc[i][threadIdx.x];
+        }
+        a.counts[static_cast<int64_t>(s) * E + e] = cs;
+        a.probs[static_cast<int64_t>(s) * E + e] = static_cast<float>(ps);
+        dot = cs * ps;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         dot += __shfl_xor_sync(kAll, dot, o);
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.0;
-        for (int w = 0; w < kWarps; ++w)
-            dot += red[w];
+    if (threadIdx.x != 0)
+        return;
+    if (blockIdx.x == 0)
         a.tokens[s] = n;
-        a.loss[s] = n == 0 ? 0.0f : static_cast<float>(dot * E / (static_cast<double>(a.k) * n * n));
+    const int blocks = gridDim.x;
+    if (n == 0) {
+        if (blockIdx.x == 0)
+            a.loss[s] = 0.0f;
+        return;
     }
+    if (blocks > 1) {
+        // (a sequence with tokens has chunks, so its counter was set to 0)
+        a.part_dot[static_cast<int64_t>(s) * blocks + blockIdx.x] = dot;
+        __threadfence();
+        last_s = atomicAdd(a.done + s, 1) == blocks - 1;
+        if (!last_s)
+            return;
+        __threadfence();
+        dot = 0.0;
+        for (int i = 0; i < blocks; ++i)
+            dot += __ldcg(a.part_dot + static_cast<int64_t>(s) * blocks + i);
+    }
+    a.loss[s] = static_cast<float>(dot * E / (static_cast<double>(a.k) * n * n));
 }
 
 // Gradient: one warp per token, consecutive tokens per warp.
 template <int P, bool V4>
-__global__ void __launch_bounds__(kThreads) balance_backward_kernel(const BalanceArgs a, int per_warp)
+__global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward_kernel(const BalanceArgs a, int per_warp)
 {
-    extern __shared__ float sm[];                 // [kWarps][E]: the weights' part of a row
+    extern __shared__ __align__(16) float sm[];   // [kWarps][E]: the weights' part of a row
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -252,9 +404,40 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
     if (tw >= a.T)
         return;
     const int t_end = static_cast<int>(min(tw + per_warp, a.T));
+    // The sequence's counts stay in registers for rows of up to 384 columns;
+    // longer rows read them again for every token (from L1), which leaves
+    // registers for twice the warps.
+    constexpr bool kHold = P <= 3;
     int s = -1, s_end = 0;
-    float cnt[4 * P], coef = 0.0f;
-    for (int t = static_cast<int>(tw); t < t_end; ++t) {
+    float cnt[kHold ? 4 * P : 1] = {}, coef = 0.0f;
+    auto count = [&](int q) -> float {
+        if (kHold)
+            return cnt[kHold ? q : 0];
+        const int c = Row<P, V4>::col(lane, q);
+        return c < E ? static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
+    };
+    constexpr int D = tokens_ahead(P);
+    Row<P, V4> ring[D];
+    int ids[D];
+    float grads[D];                                // slot lane's weight gradient
+    auto fetch = [&](int u, int t) {
+        if (t < t_end) {
+            ids[u] = raw_id(a, t, lane);
+            ring[u].load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+            grads[u] = a.grad_weights != nullptr && lane < a.k
+                           ? __ldg(a.grad_weights + static_cast<int64_t>(t) * a.k + lane)
+                           : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        fetch(u, static_cast<int>(tw) + u);
+    for (int tb = static_cast<int>(tw); tb < t_end; tb += D)
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+        const int t = tb + u;
+        if (t >= t_end)
+            break;
         if (s < 0 || t >= s_end) {
             // the last sequence that starts at or before t (and is not empty there)
             int lo = 0, hi = a.S;
@@ -272,60 +455,79 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
             coef = in ? static_cast<float>(static_cast<double>(__ldg(a.grad_loss + s)) * E /
                                            (static_cast<double>(a.k) * n * n))
                       : 0.0f;
+            if (kHold)
 #pragma unroll
-            for (int q = 0; q < 4 * P; ++q) {
-                const int c = Row<P, V4>::col(lane, q);
-                cnt[q] = in && c < E ? static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
-            }
+                for (int q = 0; q < 4 * P; ++q) {
+                    const int c = Row<P, V4>::col(lane, q);
+                    cnt[kHold ? q : 0] =
+                        in && c < E ? static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
+                }
             if (!in)
                 s = -1;                            // outside every sequence: looked up again for the next token
         }
         float *out = a.grad_logits + static_cast<int64_t>(t) * E;
-        const int id = lane < a.k && s >= 0 ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
-        const bool on = id >= 0 && id < E;
-        Row<P, V4> r;
+        Row<P, V4> r = ring[u];
+        const int id = ids[u];
+        const float g = grads[u];
+        const bool on = s >= 0 && id >= 0 && id < E;
+        // (from L1: the row has just been read)
+        const float l = on && a.grad_weights != nullptr ? __ldg(a.logits + static_cast<int64_t>(t) * E + id) : 0.0f;
+        fetch(u, t + D);
         if (__any_sync(kAll, on)) {
-            const float *row = a.logits + static_cast<int64_t>(t) * E;
-            r.load(row, E, lane);
             const float inv = r.scores(a.scoring);
             float dot = 0.0f;
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q)
-                dot = fmaf(r.v[q], cnt[q], dot);
+                dot = fmaf(r.v[q], count(q), dot);
             dot = warp_sum(dot) * inv;
             const float ci = coef * inv;
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q) {
                 const float sc = r.v[q];
-                r.v[q] = ci * sc * (cnt[q] - dot);
+                r.v[q] = ci * sc * (count(q) - dot);
                 if (a.scoring != NVFP4_SCORING_SOFTMAX)
                     r.v[q] *= 1.0f - sc;
             }
             if (a.grad_weights != nullptr) {
-                const float l = on ? __ldg(row + id) : -INFINITY;
                 float v, slope = 1.0f;
                 if (a.scoring == NVFP4_SCORING_SOFTMAX) {
-                    const float m = warp_max(l);
-                    v = on && m != -INFINITY ? expf(l - m) : 0.0f;
+                    const float m = warp_max(on ? l : -INFINITY);
+                    v = on && m != -INFINITY ? exp_fast(l - m) : 0.0f;
                 } else {
-                    v = on ? __frcp_rn(1.0f + expf(-l)) : 0.0f;
+                    v = on ? sigmoid_fast(l) : 0.0f;
                     slope = 1.0f - v;
                 }
                 const float sum = warp_sum(v);
                 const float w = sum == 0.0f ? 0.0f : __fdiv_rn(v, sum);
-                const float g = on ? __ldg(a.grad_weights + static_cast<int64_t>(t) * a.k + lane) : 0.0f;
-                const float d = w * (g - warp_sum(g * w)) * slope;
-                // slots of one expert add up in slot order
-                for (int j = 0; j < a.k; ++j) {
-                    if (lane == j && on)
-                        extra[id] += d;
-                    __syncwarp();
+                const float d = w * (g - warp_sum(on ? g * w : 0.0f)) * slope;
+                // into the row by way of shared memory; slots of one expert add up in slot order
+                const unsigned twins = __match_any_sync(kAll, on ? id : -1 - lane);
+                if (!__any_sync(kAll, (twins & (twins - 1)) != 0)) {
+                    if (on)
+                        extra[id] = d;
+                } else {
+                    for (int j = 0; j < a.k; ++j) {
+                        if (lane == j && on)
+                            extra[id] += d;
+                        __syncwarp();
+                    }
                 }
+                __syncwarp();
+                if (V4) {
 #pragma unroll
-                for (int q = 0; q < 4 * P; ++q) {
-                    const int c = Row<P, V4>::col(lane, q);
-                    if (c < E)
-                        r.v[q] += extra[c];
+                    for (int i = 0; i < P; ++i) {
+                        const int c = 4 * (lane + 32 * i);
+                        const float4 f =
+                            c < E ? *reinterpret_cast<const float4 *>(extra + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        r.v[4 * i] += f.x, r.v[4 * i + 1] += f.y, r.v[4 * i + 2] += f.z, r.v[4 * i + 3] += f.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4 * P; ++q) {
+                        const int c = Row<P, V4>::col(lane, q);
+                        if (c < E)
+                            r.v[q] += extra[c];
+                    }
                 }
                 __syncwarp();
                 if (on)
@@ -351,15 +553,24 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
     }
 }
 
-int balance_chunk(int64_t T)
+// Tokens per chunk: about as many chunks as blocks fit on the 148 SMs of the
+// device (more, shorter ones pay each block's start and end; fewer leave SMs
+// idle), but a token per warp at least.
+int balance_chunk(int64_t T, int E)
 {
-    const int64_t c = (T + 511) / 512;
-    return static_cast<int>(c < 8 ? 8 : c);
+    const int64_t blocks = 148 * chunk_blocks((E + 127) / 128);
+    const int64_t c = (T + blocks - 1) / blocks;
+    return static_cast<int>(c < kWarps ? kWarps : c);
 }
 
-int64_t balance_slots(int64_t T, int64_t S)
+int balance_sum_blocks(int E)
 {
-    return T / balance_chunk(T) + S;
+    return (E + kCols - 1) / kCols;
+}
+
+int64_t balance_slots(int64_t T, int64_t S, int E)
+{
+    return T / balance_chunk(T, E) + S;
 }
 
 // 16-byte loads and stores need every row to start on a 16-byte boundary.
@@ -381,16 +592,29 @@ namespace {
 template <int P, bool V4>
 cudaError_t chunk_launch(const BalanceArgs &a, cudaStream_t s)
 {
-    return launch_pdl(balance_chunk_kernel<P, V4>, dim3(static_cast<unsigned>(balance_slots(a.T, a.S))),
+    return launch_pdl(balance_chunk_kernel<P, V4, false>, dim3(static_cast<unsigned>(balance_slots(a.T, a.S, a.E))),
                       dim3(kThreads), sizeof(float) * (kWarps + 1) * a.E, s, a);
+}
+
+template <int P, bool V4>
+cudaError_t whole_launch(const BalanceArgs &a, cudaStream_t s)
+{
+    static unsigned long long attr_done = 0;
+    constexpr int W = kWholeThreads / 32;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(balance_chunk_kernel<P, V4, true>),
+                                            sizeof(float) * (W + 1) * 1024, &attr_done);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(balance_chunk_kernel<P, V4, true>, dim3(static_cast<unsigned>(a.S)), dim3(kWholeThreads),
+                      sizeof(float) * (W + 1) * a.E, s, a);
 }
 
 template <int P, bool V4>
 cudaError_t backward_launch(const BalanceArgs &a, cudaStream_t s)
 {
-    int64_t per = (a.T + 148 * 32 - 1) / (148 * 32);
-    if (per < 1)
-        per = 1;
+    // consecutive tokens per warp, one wave of blocks
+    const int64_t warps = 148LL * kWarps * backward_blocks(P);
+    const int64_t per = (a.T + warps - 1) / warps;
     const int64_t grid = (a.T + kWarps * per - 1) / (kWarps * per);
     return launch_pdl(balance_backward_kernel<P, V4>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
                       sizeof(float) * kWarps * a.E, s, a, static_cast<int>(per));
@@ -403,14 +627,25 @@ cudaError_t launch_chunks(const BalanceArgs &a, cudaStream_t s)
 #undef F
 }
 
+cudaError_t launch_whole(const BalanceArgs &a, cudaStream_t s)
+{
+#define F(P, V) whole_launch<P, V>(a, s)
+    NVFP4_BALANCE_CASES(F)
+#undef F
+}
+
 } // namespace
 
 cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t s)
 {
-    cudaError_t e = a.T > 0 ? launch_chunks(a, s) : cudaSuccess;
-    if (e == cudaSuccess)
-        e = launch_pdl(balance_sum_kernel, dim3(static_cast<unsigned>(a.S)), dim3(kThreads), 0, s, a);
-    return e;
+    if (a.T <= kWholeTokens)
+        return launch_whole(a, s);
+    const cudaError_t e = launch_chunks(a, s);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(balance_sum_kernel,
+                      dim3(static_cast<unsigned>(balance_sum_blocks(a.E)), static_cast<unsigned>(a.S)), dim3(kThreads),
+                      0, s, a);
 }
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, cudaStream_t s)

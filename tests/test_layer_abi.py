@@ -109,7 +109,7 @@ def backward(L, **kw):
 SHARED = [
     (dict(logits=None), -1), (dict(ids=None), -1), (dict(T=-1), -1), (dict(E=0), -1), (dict(k=0), -1), (dict(ld=5), -1),
     (dict(S=0), -1), (dict(scoring=2), -1), (dict(off=None), -1), (dict(counts=None), -1), (dict(tokens=None), -1),
-    (dict(E=1025), -2), (dict(k=33, ld=33), -2), (dict(E=4), -2), (dict(T=1 << 31), -2), (dict(S=(1 << 24) + 1), -2),
+    (dict(E=1025), -2), (dict(k=33, ld=33), -2), (dict(E=4), -2), (dict(T=1 << 31), -2), (dict(S=65536), -2),
 ]
 
 
