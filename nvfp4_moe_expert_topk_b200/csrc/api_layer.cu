@@ -197,7 +197,7 @@ int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_i
     a.S = static_cast<int>(S);
     a.offsets = seq_offsets;
     a.scoring = scoring;
-    a.chunk = balance_chunk(T, E);
+    a.chunk = balance_chunk(T, S, E);
     a.counts = counts;
     a.tokens = tokens;
     a.probs = probs;

@@ -48,20 +48,38 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// Sums over the warp of four values at once (each lane gets all four): the
+// first two exchanges halve the values a lane carries, so that ten exchanges
+// do what four separate sums take twenty for, in six dependent steps.
+__device__ __forceinline__ void warp_sum4(float (&v)[4])
+{
+    const int lane = threadIdx.x & 31;
+    const bool up16 = (lane & 16) != 0, up8 = (lane & 8) != 0;
+    const float a = (up16 ? v[2] : v[0]) + __shfl_xor_sync(kAll, up16 ? v[0] : v[2], 16);
+    const float b = (up16 ? v[3] : v[1]) + __shfl_xor_sync(kAll, up16 ? v[1] : v[3], 16);
+    float s = (up8 ? b : a) + __shfl_xor_sync(kAll, up8 ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        s += __shfl_xor_sync(kAll, s, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)                    // value i is in the lanes 8 i .. 8 i + 7
+        v[i] = __shfl_sync(kAll, s, 8 * i);
+}
+
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
 // exp(x), x <= 0 or moderate: 2^(x log2 e) on the special-function unit, off by
-// 2 ulp and by the rounding of the product (|x| 2^-24 relative).
+// 2 ulp and by the rounding of the product (|x| 2^-24 relative); results below
+// 2^-126 are 0.
 __device__ __forceinline__ float exp_fast(float x)
 {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
     return y;
 }
 
@@ -69,7 +87,7 @@ __device__ __forceinline__ float exp_fast(float x)
 __device__ __forceinline__ float rcp_fast(float x)
 {
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -90,6 +108,21 @@ __device__ __forceinline__ int seq_start(const BalanceArgs &a, int s)
 __device__ __forceinline__ int first_slot(const BalanceArgs &a, int s)
 {
     return seq_start(a, s) / a.chunk + s;
+}
+
+// The last s in [0, S) with before(s), where before holds up to some s (and is
+// taken to hold for 0); the whole warp looks at 32 places at a time.
+template <typename F>
+__device__ __forceinline__ int last_sequence(int S, int lane, F before)
+{
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const int n = __popc(__ballot_sync(kAll, at < hi && (at == lo || before(at))));
+        lo += (n - 1) * step;
+        hi = min(lo + step, hi);
+    }
+    return lo;
 }
 
 // Tokens [t0, t1) of chunk slot `slot` of sequence s (empty: t0 >= t1).
@@ -117,8 +150,10 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int c = 4 * (lane + 32 * i);
-                const float4 f = c < E ? __ldg(reinterpret_cast<const float4 *>(row + c))
-                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                // (P is E / 128 rounded up, up to 4: only the last piece can be short)
+                const bool in = (P <= 4 && i < P - 1) || c < E;
+                const float4 f = in ? __ldg(reinterpret_cast<const float4 *>(row + c))
+                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
                 v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
             }
         } else {
@@ -127,12 +162,13 @@ struct Row {
                 v[q] = col(lane, q) < E ? __ldg(row + col(lane, q)) : -INFINITY;
         }
     }
-    // scores (exp(l - max) or sigmoid(l)) in place; returns 1 / their sum, or 0
-    // where the sum is 0 (a row of -inf: no probability anywhere)
-    __device__ __forceinline__ float scores(int scoring)
+    // scores (exp(l - max) or sigmoid(l)) in place; returns the lane's part of
+    // their sum (which is 0 for a row of -inf: no probability anywhere)
+    template <bool SIG>
+    __device__ __forceinline__ float scores()
     {
         float sum = 0.0f;
-        if (scoring == NVFP4_SCORING_SOFTMAX) {
+        if (!SIG) {
             float m = v[0];
 #pragma unroll
             for (int q = 1; q < 4 * P; ++q)
@@ -152,33 +188,32 @@ struct Row {
                 sum += v[q];
             }
         }
-        sum = warp_sum(sum);
-        return sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        return sum;
     }
 };
 
-} // namespace
-
-// Slot lane's id as stored (read ahead: checked when it is used).
-__device__ __forceinline__ int raw_id(const BalanceArgs &a, int t, int lane)
+// 1 / x, 0 for 0.
+__device__ __forceinline__ float inverse(float x)
 {
-    return lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
+    return x == 0.0f ? 0.0f : __frcp_rn(x);
 }
 
-// Tokens a warp has on their way: short rows need several to fill the memory's
-// latency, a long row is enough by itself.
-__host__ __device__ constexpr int tokens_ahead(int P) { return P == 1 ? 4 : P == 2 ? 2 : 1; }
+} // namespace
+
+// Tokens a warp holds at a time: one is worked on in place while the others are
+// on their way (short rows need several to fill the memory's latency).
+__host__ __device__ constexpr int tokens_held(int P) { return P == 1 ? 4 : 2; }
 
 // Blocks per SM, by the registers that a row of up to 128 P columns takes.
 __host__ __device__ constexpr int chunk_blocks(int P) { return P <= 3 ? 4 : P <= 4 ? 3 : 2; }
-__host__ __device__ constexpr int backward_blocks(int P) { return P <= 3 ? 3 : 2; }
+__host__ __device__ constexpr int backward_blocks(int P) { return P <= 2 ? 4 : P <= 3 ? 3 : 2; }
 
 // Sums of a run of tokens of one sequence: a chunk's, left in the workspace, or
 // (WHOLE, short batches) a whole sequence's, with its loss, in one launch.
-template <int P, bool V4, bool WHOLE>
+template <int P, bool V4, bool SIG, bool WHOLE>
 __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : chunk_blocks(P)) balance_chunk_kernel(const BalanceArgs a)
 {
-    constexpr int W = (WHOLE ? kWholeThreads : kThreads) / 32, D = tokens_ahead(P);
+    constexpr int W = (WHOLE ? kWholeThreads : kThreads) / 32, D = tokens_held(P);
     extern __shared__ float sm[];                 // [W][E] probability sums, then [E] int counts
     __shared__ int tokens_s;
     __shared__ double red[W];
@@ -192,16 +227,7 @@ __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : 
         t0 = seq_start(a, seq);
         t1 = seq_start(a, seq + 1);
     } else {
-        // the last sequence whose first slot is <= slot
-        int lo = 0, hi = a.S;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (first_slot(a, mid) <= slot)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        seq = lo;
+        seq = last_sequence(a.S, lane, [&](int s) { return first_slot(a, s) <= slot; });
         slot_tokens(a, seq, slot, t0, t1);
         if (t0 >= t1)
             return;
@@ -209,15 +235,21 @@ __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : 
     // (a padded token's logits are not used, but they are there to be read)
     Row<P, V4> ring[D];
     int ids[D];
-    auto fetch = [&](int u, int t) {
-        if (t < t1) {
-            ids[u] = raw_id(a, t, lane);
-            ring[u].load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+    int tf = t0 + warp;                            // next token to fetch, its row and its ids
+    const float *lf = a.logits + static_cast<int64_t>(tf) * E;
+    const int32_t *idf = a.ids + static_cast<int64_t>(tf) * a.ld_ids + lane;
+    auto fetch = [&](int u) {
+        if (tf < t1) {
+            ids[u] = lane < a.k ? __ldg(idf) : -1;
+            ring[u].load(lf, E, lane);
         }
+        tf += W;
+        lf += W * E;
+        idf += W * a.ld_ids;
     };
 #pragma unroll
     for (int u = 0; u < D; ++u)
-        fetch(u, t0 + warp + u * W);
+        fetch(u);
     int *hist = reinterpret_cast<int *>(sm + W * E);
     for (int e = threadIdx.x; e < E; e += 32 * W)
         hist[e] = 0;
@@ -235,19 +267,19 @@ __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : 
             const int t = tb + u * W;
             if (t >= t1)
                 break;
-            Row<P, V4> r = ring[u];
+            Row<P, V4> &r = ring[u];
             const int id = ids[u];
             const bool on = id >= 0 && id < E;
-            fetch(u, t + D * W);
-            if (!__any_sync(kAll, on))
-                continue;                          // a padded token
-            ++tokens;
-            if (on)
-                atomicAdd(hist + id, 1);
-            const float inv = r.scores(a.scoring);
+            if (__any_sync(kAll, on)) {            // not a padded token
+                ++tokens;
+                if (on)
+                    atomicAdd(hist + id, 1);
+                const float inv = inverse(warp_sum(r.template scores<SIG>()));
 #pragma unroll
-            for (int q = 0; q < 4 * P; ++q)
-                acc[q] = fmaf(r.v[q], inv, acc[q]);
+                for (int q = 0; q < 4 * P; ++q)
+                    acc[q] = fmaf(r.v[q], inv, acc[q]);
+            }
+            fetch(u);
         }
     }
     if (lane == 0 && tokens)
@@ -389,7 +421,7 @@ __global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalanceArgs
 }
 
 // Gradient: one warp per token, consecutive tokens per warp.
-template <int P, bool V4>
+template <int P, bool V4, bool SIG>
 __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward_kernel(const BalanceArgs a, int per_warp)
 {
     extern __shared__ __align__(16) float sm[];   // [kWarps][E]: the weights' part of a row
@@ -404,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
     if (tw >= a.T)
         return;
     const int t_end = static_cast<int>(min(tw + per_warp, a.T));
-    // The sequence's counts stay in registers for rows of up to 384 columns;
+    // The sequence's counts (times its coefficient) stay in registers for rows of up to 384 columns;
     // longer rows read them again for every token (from L1), which leaves
     // registers for twice the warps.
     constexpr bool kHold = P <= 3;
@@ -414,24 +446,25 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
         if (kHold)
             return cnt[kHold ? q : 0];
         const int c = Row<P, V4>::col(lane, q);
-        return c < E ? static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
+        return c < E ? coef * static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
     };
-    constexpr int D = tokens_ahead(P);
+    constexpr int D = tokens_held(P);
     Row<P, V4> ring[D];
     int ids[D];
     float grads[D];                                // slot lane's weight gradient
-    auto fetch = [&](int u, int t) {
+    int64_t at = tw * E, id_at = tw * a.ld_ids + lane;         // the current token's row and its slot lane
+    auto fetch = [&](int u, int ahead, int t) {
         if (t < t_end) {
-            ids[u] = raw_id(a, t, lane);
-            ring[u].load(a.logits + static_cast<int64_t>(t) * E, E, lane);
+            ids[u] = lane < a.k ? __ldg(a.ids + id_at + ahead * a.ld_ids) : -1;
             grads[u] = a.grad_weights != nullptr && lane < a.k
                            ? __ldg(a.grad_weights + static_cast<int64_t>(t) * a.k + lane)
                            : 0.0f;
+            ring[u].load(a.logits + at + ahead * E, E, lane);
         }
     };
 #pragma unroll
     for (int u = 0; u < D; ++u)
-        fetch(u, static_cast<int>(tw) + u);
+        fetch(u, u, static_cast<int>(tw) + u);
     for (int tb = static_cast<int>(tw); tb < t_end; tb += D)
 #pragma unroll
     for (int u = 0; u < D; ++u) {
@@ -440,15 +473,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
             break;
         if (s < 0 || t >= s_end) {
             // the last sequence that starts at or before t (and is not empty there)
-            int lo = 0, hi = a.S;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (seq_start(a, mid) <= t)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            s = lo;
+            s = last_sequence(a.S, lane, [&](int i) { return seq_start(a, i) <= t; });
             s_end = seq_start(a, s + 1);
             const int n = __ldg(a.tokens + s);
             const bool in = t >= seq_start(a, s) && t < s_end && n > 0;
@@ -460,49 +485,57 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
                 for (int q = 0; q < 4 * P; ++q) {
                     const int c = Row<P, V4>::col(lane, q);
                     cnt[kHold ? q : 0] =
-                        in && c < E ? static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
+                        in && c < E ? coef * static_cast<float>(__ldg(a.counts + static_cast<int64_t>(s) * E + c)) : 0.0f;
                 }
             if (!in)
                 s = -1;                            // outside every sequence: looked up again for the next token
         }
-        float *out = a.grad_logits + static_cast<int64_t>(t) * E;
-        Row<P, V4> r = ring[u];
+        Row<P, V4> &r = ring[u];
         const int id = ids[u];
         const float g = grads[u];
         const bool on = s >= 0 && id >= 0 && id < E;
         // (from L1: the row has just been read)
-        const float l = on && a.grad_weights != nullptr ? __ldg(a.logits + static_cast<int64_t>(t) * E + id) : 0.0f;
-        fetch(u, t + D);
+        const float l = on && a.grad_weights != nullptr ? __ldg(a.logits + at + id) : 0.0f;
         if (__any_sync(kAll, on)) {
-            const float inv = r.scores(a.scoring);
-            float dot = 0.0f;
+            // the row's scores, and the selected slots' for the weights' part
+            float sums[4];
+            sums[0] = r.template scores<SIG>();
+            sums[1] = 0.0f;
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q)
-                dot = fmaf(r.v[q], count(q), dot);
-            dot = warp_sum(dot) * inv;
-            const float ci = coef * inv;
-#pragma unroll
-            for (int q = 0; q < 4 * P; ++q) {
-                const float sc = r.v[q];
-                r.v[q] = ci * sc * (count(q) - dot);
-                if (a.scoring != NVFP4_SCORING_SOFTMAX)
-                    r.v[q] *= 1.0f - sc;
-            }
+                sums[1] = fmaf(r.v[q], count(q), sums[1]);
+            float v = 0.0f, slope = 1.0f;
             if (a.grad_weights != nullptr) {
-                float v, slope = 1.0f;
-                if (a.scoring == NVFP4_SCORING_SOFTMAX) {
+                if (!SIG) {
                     const float m = warp_max(on ? l : -INFINITY);
                     v = on && m != -INFINITY ? exp_fast(l - m) : 0.0f;
                 } else {
                     v = on ? sigmoid_fast(l) : 0.0f;
                     slope = 1.0f - v;
                 }
-                const float sum = warp_sum(v);
-                const float w = sum == 0.0f ? 0.0f : __fdiv_rn(v, sum);
-                const float d = w * (g - warp_sum(on ? g * w : 0.0f)) * slope;
+            }
+            sums[2] = v;
+            sums[3] = on ? g * v : 0.0f;
+            warp_sum4(sums);
+            // p (c - sum p c) coef with p = score * inv and the counts scaled by coef: score (inv c' - inv dot)
+            const float inv = inverse(sums[0]);
+            const float dot = -sums[1] * inv * inv;
+#pragma unroll
+            for (int q = 0; q < 4 * P; ++q) {
+                const float sc = r.v[q];
+                r.v[q] = sc * fmaf(inv, count(q), dot);
+                if (SIG)
+                    r.v[q] *= 1.0f - sc;
+            }
+            if (a.grad_weights != nullptr) {
+                // w (g - sum g w) with w = v / sum v
+                const float q = inverse(sums[2]);
+                const float d = v * q * (g - sums[3] * q) * slope;
                 // into the row by way of shared memory; slots of one expert add up in slot order
-                const unsigned twins = __match_any_sync(kAll, on ? id : -1 - lane);
-                if (!__any_sync(kAll, (twins & (twins - 1)) != 0)) {
+                bool twin = false;
+                for (int j = 0; j + 1 < a.k; ++j)
+                    twin |= __shfl_sync(kAll, id, j) == id && lane > j;
+                if (!__any_sync(kAll, twin && on)) {
                     if (on)
                         extra[id] = d;
                 } else {
@@ -544,21 +577,25 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
             const int c = Row<P, V4>::col(lane, V4 ? 4 * i : i);
             if (c < E) {
                 if (V4)
-                    *reinterpret_cast<float4 *>(out + c) =
+                    *reinterpret_cast<float4 *>(a.grad_logits + at + c) =
                         make_float4(r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]);
                 else
-                    out[c] = r.v[i];
+                    a.grad_logits[at + c] = r.v[i];
             }
         }
+        fetch(u, D, t + D);
+        at += E;
+        id_at += a.ld_ids;
     }
 }
 
 // Tokens per chunk: about as many chunks as blocks fit on the 148 SMs of the
 // device (more, shorter ones pay each block's start and end; fewer leave SMs
 // idle), but a token per warp at least.
-int balance_chunk(int64_t T, int E)
+int balance_chunk(int64_t T, int64_t S, int E)
 {
-    const int64_t blocks = 148 * chunk_blocks((E + 127) / 128);
+    const int64_t fit = 148 * chunk_blocks((E + 127) / 128);
+    const int64_t blocks = S < fit / 2 ? fit - S : fit / 2;    // (every sequence may add a chunk)
     const int64_t c = (T + blocks - 1) / blocks;
     return static_cast<int>(c < kWarps ? kWarps : c);
 }
@@ -570,7 +607,7 @@ int balance_sum_blocks(int E)
 
 int64_t balance_slots(int64_t T, int64_t S, int E)
 {
-    return T / balance_chunk(T, E) + S;
+    return T / balance_chunk(T, S, E) + S;
 }
 
 // 16-byte loads and stores need every row to start on a 16-byte boundary.
@@ -579,57 +616,59 @@ static bool aligned_rows(const BalanceArgs &a)
     return ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.grad_logits)) & 15) == 0;
 }
 
+// F(P, V4, SIG) of the smallest P that holds a row.
+#define NVFP4_BALANCE_ROWS(F, V, S)                                                                              \
+    (p4 <= 1 ? F(1, V, S) : p4 <= 2 ? F(2, V, S) : p4 <= 3 ? F(3, V, S) : p4 <= 4 ? F(4, V, S) : F(8, V, S))
 #define NVFP4_BALANCE_CASES(F)                                                                                   \
     const int p4 = (a.E + 127) / 128;                                                                            \
     const bool v4 = a.E % 4 == 0 && aligned_rows(a);                                                             \
-    if (v4)                                                                                                      \
-        return p4 <= 1 ? F(1, true) : p4 <= 2 ? F(2, true) : p4 <= 3 ? F(3, true) : p4 <= 4 ? F(4, true)         \
-               : F(8, true);                                                                                     \
-    return p4 <= 1 ? F(1, false) : p4 <= 3 ? F(3, false) : F(8, false);
+    if (a.scoring == NVFP4_SCORING_SOFTMAX)                                                                      \
+        return v4 ? NVFP4_BALANCE_ROWS(F, true, false) : NVFP4_BALANCE_ROWS(F, false, false);                    \
+    return v4 ? NVFP4_BALANCE_ROWS(F, true, true) : NVFP4_BALANCE_ROWS(F, false, true);
 
 namespace {
 
-template <int P, bool V4>
+template <int P, bool V4, bool SIG>
 cudaError_t chunk_launch(const BalanceArgs &a, cudaStream_t s)
 {
-    return launch_pdl(balance_chunk_kernel<P, V4, false>, dim3(static_cast<unsigned>(balance_slots(a.T, a.S, a.E))),
+    return launch_pdl(balance_chunk_kernel<P, V4, SIG, false>, dim3(static_cast<unsigned>(balance_slots(a.T, a.S, a.E))),
                       dim3(kThreads), sizeof(float) * (kWarps + 1) * a.E, s, a);
 }
 
-template <int P, bool V4>
+template <int P, bool V4, bool SIG>
 cudaError_t whole_launch(const BalanceArgs &a, cudaStream_t s)
 {
     static unsigned long long attr_done = 0;
     constexpr int W = kWholeThreads / 32;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(balance_chunk_kernel<P, V4, true>),
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(balance_chunk_kernel<P, V4, SIG, true>),
                                             sizeof(float) * (W + 1) * 1024, &attr_done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(balance_chunk_kernel<P, V4, true>, dim3(static_cast<unsigned>(a.S)), dim3(kWholeThreads),
+    return launch_pdl(balance_chunk_kernel<P, V4, SIG, true>, dim3(static_cast<unsigned>(a.S)), dim3(kWholeThreads),
                       sizeof(float) * (W + 1) * a.E, s, a);
 }
 
-template <int P, bool V4>
+template <int P, bool V4, bool SIG>
 cudaError_t backward_launch(const BalanceArgs &a, cudaStream_t s)
 {
     // consecutive tokens per warp, one wave of blocks
     const int64_t warps = 148LL * kWarps * backward_blocks(P);
     const int64_t per = (a.T + warps - 1) / warps;
     const int64_t grid = (a.T + kWarps * per - 1) / (kWarps * per);
-    return launch_pdl(balance_backward_kernel<P, V4>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+    return launch_pdl(balance_backward_kernel<P, V4, SIG>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
                       sizeof(float) * kWarps * a.E, s, a, static_cast<int>(per));
 }
 
 cudaError_t launch_chunks(const BalanceArgs &a, cudaStream_t s)
 {
-#define F(P, V) chunk_launch<P, V>(a, s)
+#define F(P, V, S) chunk_launch<P, V, S>(a, s)
     NVFP4_BALANCE_CASES(F)
 #undef F
 }
 
 cudaError_t launch_whole(const BalanceArgs &a, cudaStream_t s)
 {
-#define F(P, V) whole_launch<P, V>(a, s)
+#define F(P, V, S) whole_launch<P, V, S>(a, s)
     NVFP4_BALANCE_CASES(F)
 #undef F
 }
@@ -650,7 +689,7 @@ cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t s)
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, cudaStream_t s)
 {
-#define F(P, V) backward_launch<P, V>(a, s)
+#define F(P, V, S) backward_launch<P, V, S>(a, s)
     NVFP4_BALANCE_CASES(F)
 #undef F
 }

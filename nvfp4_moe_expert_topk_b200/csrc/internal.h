@@ -244,7 +244,7 @@ struct BalanceArgs {
     const float *grad_loss, *grad_weights;
     float *grad_logits;
 };
-int balance_chunk(int64_t T, int E);
+int balance_chunk(int64_t T, int64_t S, int E);
 int64_t balance_slots(int64_t T, int64_t S, int E);
 int balance_sum_blocks(int E);
 cudaError_t launch_balance(const BalanceArgs &args, cudaStream_t s);
