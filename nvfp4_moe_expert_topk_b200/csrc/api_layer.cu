@@ -102,6 +102,7 @@ int nvfp4_add_rmsnorm(const nvfp4_norm_args *a, void *stream)
     n.ldy = a->ldy;
     n.T = a->T;
     n.nb = static_cast<int>(a->H / 16);
+    n.inv_cols = 1.0 / static_cast<double>(a->H);
     n.eps = a->eps;
     n.quant = a->quant;
     n.layout = a->scale_layout;

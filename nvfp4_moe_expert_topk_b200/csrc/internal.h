@@ -201,7 +201,7 @@ struct NormArgs {
     int64_t ldx, ldr, ldro, ldy;
     int64_t T;
     int nb;                   // H / 16
-    double eps;
+    double inv_cols, eps;     // 1 / H
     int quant, layout;        // NVFP4_QUANT_*, NVFP4_SCALES_*
     const float *gs;
     uint8_t *codes;

@@ -12,6 +12,15 @@
 // residual stream.  The sum of squares is held in 64 bits: bf16 squares are
 // exact there and the sum is off by ~1e-16, so rstd, y and the codes are the
 // same bits whatever the order of summation (rows, threads, launch shape).
+//
+// Bound by HBM on long batches (10.6 bytes per element with a residual and
+// NVFP4 rows), by launch and one pass over a row on short ones: a row stays in
+// registers between its sum and its output, 16 columns per thread (one NVFP4
+// block, an eighth of an E4M3 group), several rows in flight per SM.  What is
+// exact in packed bf16 is done there: one add.bf16x2 rounds the exact sum once,
+// as fp32 addition and rounding to bf16 do (fp32 keeps 16 bits below bf16, so
+// its own rounding never moves a sum onto or over a border), and the largest
+// magnitude of a block is the largest 15-bit pattern.
 #include "internal.h"
 #include "quant.cuh"
 
@@ -40,6 +49,25 @@ __device__ __forceinline__ uint4 pack8(const float *f)
     return v;
 }
 
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint4 add8(const uint4 &a, const uint4 &b)
+{
+    return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
+}
+
+// Largest |value| of eight bf16, with the running one (bf16 pairs of magnitudes).
+__device__ __forceinline__ uint32_t max8(uint32_t m, const uint4 &v)
+{
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+    return __vmaxu2(__vmaxu2(m, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+}
+
 // fp32 pair -> two E4M3 bytes (a in the low byte), nearest even, saturating.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b)
 {
@@ -48,12 +76,48 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b)
     return r;
 }
 
+// quantize16 on sixteen bf16 values (quant.cuh), the same steps: only the
+// largest magnitude is found in packed form.
+__device__ __forceinline__ uint32_t quantize16_bf16(const uint4 &y0, const uint4 &y1, float gs, uint32_t &lo,
+                                                    uint32_t &hi)
+{
+    const uint32_t m = max8(max8(0u, y0), y1);
+    const float a = __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+    const uint32_t s = cvt_e4m3(__fmul_rn(__fdiv_rn(a, 6.0f), gs));
+    const float r = s == 0u ? 0.0f : __fdiv_rn(gs, e4m3_value(s));
+    float p[16];
+    unpack8(y0, p);
+    unpack8(y1, p + 8);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        p[i] = __fmul_rn(p[i], r);
+    lo = cvt_e2m1x8(p);
+    hi = cvt_e2m1x8(p + 8);
+    return s;
+}
+
+// fp32(1 / sqrt(m)) by way of 64 bits: two Newton steps on the fp32 estimate
+// leave 64-bit rounding errors (~2^-52), as division and square root in 64 bits
+// do at five times the instructions; values that fp32 does not hold well take
+// those.
+__device__ __forceinline__ float inverse_sqrt(double m)
+{
+    const float mf = static_cast<float>(m);
+    if (!(mf > 1e-30f && mf < 1e30f))
+        return static_cast<float>(1.0 / sqrt(m));
+    double y = rsqrtf(mf);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        y = fma(0.5 * y, fma(-m * y, y, 1.0), y);
+    return static_cast<float>(y);
+}
+
 } // namespace
 
 // `tpr` threads (a multiple of 32) per row, `blockDim.x / tpr` rows at a time;
 // thread i of a row holds the 16-column blocks i, i + tpr, ... (VPT of them).
 template <int VPT, int QUANT>
-__global__ void __launch_bounds__(512) add_rmsnorm_kernel(const NormArgs a, int tpr)
+__global__ void __launch_bounds__(512, VPT == 1 ? 3 : VPT == 2 ? 2 : 1) add_rmsnorm_kernel(const NormArgs a, int tpr)
 {
     __shared__ double part[16];
     pdl_wait();
@@ -77,16 +141,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const NormArgs a, int 
             if (a.residual != nullptr) {
                 const uint4 *rs = reinterpret_cast<const uint4 *>(a.residual + t * a.ldr + 16 * b);
                 const uint4 r0 = rs[0], r1 = rs[1];
-                float f[16], g[16];
-                unpack8(h[v][0], f);
-                unpack8(h[v][1], f + 8);
-                unpack8(r0, g);
-                unpack8(r1, g + 8);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    f[j] += g[j];
-                h[v][0] = pack8(f);
-                h[v][1] = pack8(f + 8);
+                h[v][0] = add8(h[v][0], r0);
+                h[v][1] = add8(h[v][1], r1);
                 uint4 *ro = reinterpret_cast<uint4 *>(a.residual_out + t * a.ldro + 16 * b);
                 ro[0] = h[v][0];
                 ro[1] = h[v][1];
@@ -112,7 +168,7 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const NormArgs a, int 
         for (int w = 0; w < wpr; ++w)
             sum += part[row_in_block * wpr + w];
     }
-    const float rstd = static_cast<float>(1.0 / sqrt(sum / (16.0 * a.nb) + a.eps));
+    const float rstd = inverse_sqrt(fma(sum, a.inv_cols, a.eps));
     const float gs = QUANT == NVFP4_QUANT_NVFP4 ? __ldg(a.gs) : 0.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -140,10 +196,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_kernel(const NormArgs a, int 
             yo[1] = y1;
         }
         if (QUANT == NVFP4_QUANT_NVFP4 && on) {
-            unpack8(y0, f);
-            unpack8(y1, f + 8);
             uint32_t lo, hi;
-            const uint32_t s = quantize16(f, gs, lo, hi);
+            const uint32_t s = quantize16_bf16(y0, y1, gs, lo, hi);
             reinterpret_cast<uint2 *>(a.codes)[t * a.nb + b] = make_uint2(lo, hi);
             uint8_t *sc = static_cast<uint8_t *>(a.scales);
             if (a.layout == NVFP4_SCALES_MMA)
