@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     constexpr int kVals = 8 * MT;                  // sums per lane and row tile
     // four accumulators in turn, so that an instruction does not wait for the previous one's sums
     constexpr int kChains = MT == 1 ? 2 : 1;
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm = sm_raw + (-smem_u32(sm_raw) & 1023u);        // (the swizzle's period; still a shared-memory address)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = pl.warps();
     const int g = lane >> 2, t = lane & 3;
     const int group = warp / pl.slices, slice = warp - group * pl.slices;
