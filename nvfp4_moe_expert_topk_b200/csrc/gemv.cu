@@ -125,14 +125,16 @@ struct GemvPlan {
     int depth;                                     // ring stages per warp
     int panel;                                     // steps of x held at a time
     int rounds;                                    // tiles per group
+    int rows;                                      // of x
     __host__ __device__ int warps() const { return groups * slices; }
     __host__ __device__ int codes() const { return warps() * depth * kCodeStage; }
     __host__ __device__ int ring() const { return codes() + warps() * depth * kScaleStage; }
-    __host__ __device__ int x(int mt) const { return panel * mt * 4096; }
+    __host__ __device__ int step_x() const { return rows * kStep * 2; }
+    __host__ __device__ int x() const { return panel * step_x(); }
     __host__ __device__ int red(int mt) const { return slices > 1 ? warps() * mt * 1024 : 0; }
     __host__ __device__ int owned() const { return (rounds + cluster - 1) / cluster; }
     __host__ __device__ int sums(int mt) const { return cluster > 1 ? cluster * owned() * groups * mt * 1024 : 0; }
-    __host__ __device__ int total(int mt) const { return ring() + x(mt) + red(mt) + sums(mt); }
+    __host__ __device__ int total(int mt) const { return ring() + x() + red(mt) + sums(mt); }
 };
 
 // The launch's tensor maps: codes as [N / 32][32][K / 2] (whole blocks of 128
@@ -201,8 +203,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     uint8_t *codes_s = sm + warp * pl.depth * kCodeStage;
     uint8_t *scales_s = sm + pl.codes() + warp * pl.depth * kScaleStage;
     uint4 *xs = reinterpret_cast<uint4 *>(sm + pl.ring());
-    float *red = reinterpret_cast<float *>(sm + pl.ring() + pl.x(MT)) + group * pl.slices * (kVals * 32) + lane;
-    float *sums = reinterpret_cast<float *>(sm + pl.ring() + pl.x(MT) + pl.red(MT));
+    float *red = reinterpret_cast<float *>(sm + pl.ring() + pl.x()) + group * pl.slices * (kVals * 32) + lane;
+    float *sums = reinterpret_cast<float *>(sm + pl.ring() + pl.x() + pl.red(MT));
 
     // Tile of round `it` (past the last: rows that do not exist, zeros).
     auto tile_of = [&](int it) { return (it * pl.clusters + cid) * pl.groups + group; };
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
                                   : make_uint4(0, 0, 0, 0);
     };
     auto put = [&](int m, int i, const uint4 &v, uint32_t p2) {
-        xs[((i >> 2) * (MT * 4) + m * 4 + (i & 3)) * 32 + lane] =
+        xs[(i * pl.rows + 8 * m + g) * 4 + t] =
             make_uint4(to_f16x2(v.x, p2), to_f16x2(v.y, p2), to_f16x2(v.z, p2), to_f16x2(v.w, p2));
     };
     // 2^(141 - exponent) in bf16, twice
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     auto convert = [&](int p0, int n, int from) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-            if (8 * m + g < a.M) {                 // other columns hold anything: their sums are not stored
+            if (8 * m + g < a.M) {
                 const uint32_t p2 = power(m);
 #pragma unroll 4
                 for (int i = from; i < 8 * n; i += warps)
@@ -363,7 +365,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
                 if (step * kStep + 64 * t >= K)
                     s4 = make_uint4(0, 0, 0, 0);   // scales past K are not loaded
                 const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
-                const uint4 *xp = xs + (step - p0) * (2 * MT * 128) + lane;
+                const uint4 *xp[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)       // columns past M repeat row M - 1; their sums are not stored
+                    xp[m] = xs + ((step - p0) * 8 * pl.rows + min(8 * m + g, pl.rows - 1)) * 4 + t;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {      // 32 of the lane's 64 columns
                     uint32_t sc[4][2];
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
                         uint4 x[MT];
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
-                            x[m] = xp[(h * MT + m) * 128 + q * 32];
+                            x[m] = xp[m][(4 * h + q) * 4 * pl.rows];
 #pragma unroll
                         for (int p = 0; p < 2; ++p)                // rows 64 p and 64 p + 32 of the block
 #pragma unroll
@@ -554,13 +559,14 @@ static GemvPlan complete_plan(const GemvArgs &a, int groups, int slices, int clu
     p.groups = groups;
     p.slices = slices;
     p.cluster = cluster;
+    p.rows = static_cast<int>(a.M);
     const int tiles = (row_tiles + groups - 1) / groups;
     p.rounds = (tiles + fit - 1) / fit;
     p.clusters = (tiles + p.rounds - 1) / p.rounds;
     p.depth = 2;                                           // deeper beside the whole x where there is room
     const int room = kMaxBytes - p.total(mt);
-    p.depth += std::min(kMaxDepth - 2, std::max(0, (room - block_steps * mt * 4096) / (p.ring() / 2)));
-    p.panel = std::min(block_steps, (kMaxBytes - p.total(mt)) / (4096 * mt));
+    p.depth += std::min(kMaxDepth - 2, std::max(0, (room - block_steps * p.step_x()) / (p.ring() / 2)));
+    p.panel = std::min(block_steps, (kMaxBytes - p.total(mt)) / p.step_x());
     return p;
 }
 

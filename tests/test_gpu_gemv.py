@@ -131,7 +131,7 @@ def test_random_shapes(seed):
     check(M, N, K, seed=seed, seg=cuts, ldx=8 * int(rng.integers(0, 3)), ldo=int(rng.integers(0, 5)))
 
 
-@pytest.mark.parametrize("M", [2, 16])
+@pytest.mark.parametrize("M", [2, 8, 16])
 def test_long_k(M):
     """More columns than the block holds of x at a time."""
     check(M, 70, 131072 + 64, seed=1)
