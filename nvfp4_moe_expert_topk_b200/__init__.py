@@ -5,9 +5,12 @@ of libnvfp4moe.so (C ABI in include/nvfp4moe.h).  Tensors are torch CUDA
 tensors (PyTorch provides device memory and streams); each function passes
 their device pointers and the current CUDA stream to the entry point of the
 same name and raises Nvfp4Error on a non-zero status.  There is no fallback:
-if the library is missing, the first call raises.
+if the library (or, for the layer operators, the compiled marshalling module
+_binding.so) is missing, the first call raises.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -30,6 +33,7 @@ NVFP4_QUANT_NONE = 0
 NVFP4_QUANT_NVFP4 = 1
 NVFP4_QUANT_E4M3 = 2
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_binding.so")
 
 _lib = None
 
@@ -354,76 +358,28 @@ def nvfp4_debug_bounded_wait(flag, target, err, stream=None):
 
 
 # ---- operators around the routed block.  Single-token calls of these take a
-# few microseconds on the device, so their marshalling is kept short: pointers
-# travel as plain integers, the checks that pass cost one comparison each, and
-# the message is worked out only for the one that fails.  The launch goes to
-# the device of the tensors (which need not be the current one).
-_BF16, _F32, _I32, _U8, _F8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-_Tensor = torch.Tensor
+# few microseconds on the device, so their tensors are checked and passed on by
+# a compiled module (csrc/binding.cpp).  The launch goes to the device of the
+# tensors, which need not be the current one, and to that device's current
+# stream.
+_native = None
 
 
-def _refuse(dev, t, name, dtype, shape=None):
-    """Raises the ValueError that says what is wrong with `t`."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} is required" if t is None else f"{name} must be a CUDA tensor")
-    if dev is None or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor" + ("" if dev is None else f" on cuda:{dev}, got {t.device}"))
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if shape is not None:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _on(dev, t, name, dtype):
-    """Data pointer of a contiguous tensor on CUDA device `dev`."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(dev, t, name, dtype)
-
-
-def _rows_on(dev, t, name, shape):
-    """(data pointer, row stride) of a bf16 matrix whose rows may be strided."""
-    if isinstance(t, _Tensor) and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape:
-        if t.is_contiguous():
-            return t.data_ptr(), shape[1]
-        ld, step = t.stride()
-        if step == 1 or shape[1] == 1:
-            return t.data_ptr(), ld
-    _refuse(dev, t, name, _BF16, shape)
-
-
-def _first(t, name):
-    """The CUDA device index the call runs on: that of its first tensor."""
-    if isinstance(t, torch.Tensor) and t.is_cuda:
-        return t.get_device()
-    _refuse(None, t, name, None)
-
-
-def _holds(t, name, n):
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
-
-
-def _run(dev, stream, where, call, *args):
-    """call(*args, stream) with `dev` current, on `stream` or the device's
-    current stream."""
-    if stream is None:
-        raw = _raw_stream(dev)
-    else:
-        if stream.device_index != dev:
-            raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
-        raw = stream.cuda_stream
-    if dev == _current_device():
-        st = call(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            st = call(*args, raw)
-    if st != 0:
-        raise Nvfp4Error(st, where)
+def _binding():
+    """The compiled marshalling module, given the library's entry points."""
+    global _native
+    if _native is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m nvfp4_moe_expert_topk_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        L = lib()
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.nvfp4_add_rmsnorm, L.nvfp4_gemv, L.nvfp4_moe_balance, L.nvfp4_moe_balance_backward)))
+        _native = module
+    return _native
 
 
 def nvfp4_add_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, quant=NVFP4_QUANT_NONE, gs=None,
@@ -435,84 +391,23 @@ def nvfp4_add_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, 
     NVFP4_QUANT_NVFP4: gs float32 [1], codes uint8 [T, H/2], scales uint8
     (nvfp4_scales_bytes(T, H, scale_layout) bytes); NVFP4_QUANT_E4M3: codes
     uint8 or float8_e4m3fn [T, H], scales float32 [T, ceil(H/128)]."""
-    dev = _first(x, "x")
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError(f"x must be [T, H], got {list(shape)}")
-    T, H = shape
-    px, ldx = _rows_on(dev, x, "x", shape)
-    pw = _on(dev, weight, "weight", _BF16)
-    _holds(weight, "weight", H)
-    pr = po = py = pg = pc = ps = None
-    ldr = ldo = ldy = 0
-    if residual is not None and residual_out is not None:
-        pr, ldr = _rows_on(dev, residual, "residual", shape)
-        po, ldo = _rows_on(dev, residual_out, "residual_out", shape)
-    elif residual is not residual_out:
-        raise ValueError("residual and residual_out come together")
-    if y is not None:
-        py, ldy = _rows_on(dev, y, "y", shape)
-    elif quant == NVFP4_QUANT_NONE:
-        raise ValueError("y is required without a quantised output")
-    if quant == NVFP4_QUANT_NVFP4:
-        pg = _on(dev, gs, "gs", _F32)
-        pc = _on(dev, codes, "codes", _U8)
-        ps = _on(dev, scales, "scales", _U8)
-        _holds(gs, "gs", 1)
-        _holds(codes, "codes", T * (H // 2))
-        need = (T if scale_layout == NVFP4_SCALES_ROWMAJOR else T + 127 & -128) * (H // 16)
-        if scales.numel() < need:
-            raise ValueError(f"scales must hold {need} bytes, got {scales.numel()}")
-    elif quant == NVFP4_QUANT_E4M3:
-        pc = _on(dev, codes, "codes", _F8 if codes is not None and codes.dtype is _F8 else _U8)
-        ps = _on(dev, scales, "scales", _F32)
-        _holds(codes, "codes", T * H)
-        _holds(scales, "scales", T * ((H + 127) // 128))
-    _run(dev, stream, "nvfp4_add_rmsnorm", lib().nvfp4_add_rmsnorm,
-         NormArgs(px, pr, pw, T, H, ldx, ldr, ldo, ldy, eps, po, py, quant, scale_layout, pg, pc, ps))
+    st = (_native or _binding()).add_rmsnorm(x, weight, eps, y, residual, residual_out, quant, gs, codes, scales,
+                                             scale_layout, stream)
+    if st != 0:
+        raise Nvfp4Error(st, "nvfp4_add_rmsnorm")
 
 
 def nvfp4_gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
     """out bf16 [M, N] = x bf16 [M, K] (M <= 16, not quantised) x B [N, K]^T
     in NVFP4 (scales in the MMA layout, b_gs one global scale per segment of
     rows ending at seg_end); rows of x and out may be strided."""
-    dev = _first(x, "x")
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError(f"x must be [M, K], got {list(shape)}")
-    M, K = shape
-    pc = _on(dev, b_codes, "b_codes", _U8)
-    N = b_codes.shape[0]
-    px, ldx = _rows_on(dev, x, "x", shape)
-    po, ldo = _rows_on(dev, out, "out", (M, N))
-    _holds(b_codes, "b_codes", N * (K // 2))
-    ps = _on(dev, b_scales, "b_scales", _U8)
-    if b_scales.numel() < (N + 127 & -128) * (K // 16):
-        raise ValueError(f"b_scales must hold {(N + 127 & -128) * (K // 16)} bytes, got {b_scales.numel()}")
-    pg = _on(dev, b_gs, "b_gs", _F32)
-    nseg = len(seg_end)
-    _holds(b_gs, "b_gs", nseg)
-    _run(dev, stream, "nvfp4_gemv", lib().nvfp4_gemv, px, M, ldx, pc, ps, pg, (ctypes.c_int64 * nseg)(*seg_end), nseg,
-         N, K, po, ldo)
+    st = (_native or _binding()).gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream)
+    if st != 0:
+        raise Nvfp4Error(st, "nvfp4_gemv")
 
 
 def nvfp4_moe_balance_workspace_size(T, S, E):
     return int(lib().nvfp4_moe_balance_workspace_size(T, S, E))
-
-
-def _balance_inputs(logits, topk_ids, k, seq_offsets):
-    dev = _first(logits, "logits")
-    pl = _on(dev, logits, "logits", _F32)
-    pi = _on(dev, topk_ids, "topk_ids", _I32)
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [T, E], got {list(logits.shape)}")
-    T, E = logits.shape
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_ids.shape[1] < k:
-        raise ValueError(f"topk_ids must be [{T}, >= {k}], got {list(topk_ids.shape)}")
-    if seq_offsets is None:
-        return dev, pl, pi, topk_ids.shape[1], T, E, None, 1
-    po = _on(dev, seq_offsets, "seq_offsets", _I32)
-    return dev, pl, pi, topk_ids.shape[1], T, E, po, seq_offsets.numel() - 1
 
 
 def nvfp4_moe_balance(logits, topk_ids, k, counts, tokens, probs, loss, workspace, seq_offsets=None,
@@ -522,16 +417,10 @@ def nvfp4_moe_balance(logits, topk_ids, k, counts, tokens, probs, loss, workspac
     router -> counts [S, E] int32, tokens [S] int32, probs [S, E] fp32, loss
     [S] fp32; seq_offsets int32 [S + 1] (None: one sequence); workspace: uint8,
     nvfp4_moe_balance_workspace_size(T, S, E) bytes."""
-    dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
-    pc, pt = _on(dev, counts, "counts", _I32), _on(dev, tokens, "tokens", _I32)
-    pp, ps = _on(dev, probs, "probs", _F32), _on(dev, loss, "loss", _F32)
-    pw = _on(dev, workspace, "workspace", _U8)
-    _holds(counts, "counts", S * E)
-    _holds(tokens, "tokens", S)
-    _holds(probs, "probs", S * E)
-    _holds(loss, "loss", S)
-    _run(dev, stream, "nvfp4_moe_balance", lib().nvfp4_moe_balance, pl, pi, ld, T, E, k, po, S, scoring, pc, pt, pp,
-         ps, pw, workspace.numel())
+    st = (_native or _binding()).balance(logits, topk_ids, k, counts, tokens, probs, loss, workspace, seq_offsets,
+                                         scoring, stream)
+    if st != 0:
+        raise Nvfp4Error(st, "nvfp4_moe_balance")
 
 
 def nvfp4_moe_balance_backward(logits, topk_ids, k, counts, tokens, grad_loss, grad_logits, grad_weights=None,
@@ -539,16 +428,7 @@ def nvfp4_moe_balance_backward(logits, topk_ids, k, counts, tokens, grad_loss, g
     """grad_logits [T, E] fp32 = gradient of sum_s grad_loss[s] * loss[s] (and
     of sum grad_weights * topk_weights when grad_weights [T, k] is given) with
     respect to the logits; counts and tokens as nvfp4_moe_balance wrote them."""
-    dev, pl, pi, ld, T, E, po, S = _balance_inputs(logits, topk_ids, k, seq_offsets)
-    pc, pt = _on(dev, counts, "counts", _I32), _on(dev, tokens, "tokens", _I32)
-    pg, pd = _on(dev, grad_loss, "grad_loss", _F32), _on(dev, grad_logits, "grad_logits", _F32)
-    _holds(counts, "counts", S * E)
-    _holds(tokens, "tokens", S)
-    _holds(grad_loss, "grad_loss", S)
-    _holds(grad_logits, "grad_logits", T * E)
-    pw = None
-    if grad_weights is not None:
-        pw = _on(dev, grad_weights, "grad_weights", _F32)
-        _holds(grad_weights, "grad_weights", T * k)
-    _run(dev, stream, "nvfp4_moe_balance_backward", lib().nvfp4_moe_balance_backward, pl, pi, ld, T, E, k, po, S,
-         scoring, pc, pt, pg, pw, pd)
+    st = (_native or _binding()).backward(logits, topk_ids, k, counts, tokens, grad_loss, grad_logits, grad_weights,
+                                          seq_offsets, scoring, stream)
+    if st != 0:
+        raise Nvfp4Error(st, "nvfp4_moe_balance_backward")

@@ -160,3 +160,26 @@ def test_binding_refusals(L):
         pkg.nvfp4_moe_balance(torch.zeros(4, 8), None, 2, None, None, None, None, None)
     with pytest.raises(ValueError, match="logits is required"):
         pkg.nvfp4_moe_balance_backward(None, None, 2, None, None, None, None)
+
+
+def test_binding_argument_kinds(L):
+    """Arguments of another kind end in a Python error, and a refused call
+    keeps no reference to what it was given."""
+    import sys
+
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    for wrong in (3, [x], "x", object()):
+        with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+            pkg.nvfp4_add_rmsnorm(wrong, x, 1e-6, y=x)
+        with pytest.raises(ValueError, match="logits must be a CUDA tensor"):
+            pkg.nvfp4_moe_balance(wrong, x, 2, x, x, x, x, x)
+    native = pkg._binding()
+    for name, n in (("add_rmsnorm", 12), ("gemv", 7), ("balance", 11), ("backward", 11)):
+        for got in (0, n - 1, n + 1):
+            with pytest.raises(ValueError, match=f"expected {n} arguments, got {got}"):
+                getattr(native, name)(*[x] * got)
+    before = sys.getrefcount(x)
+    for _ in range(50):
+        with pytest.raises(ValueError):
+            pkg.nvfp4_add_rmsnorm(x, x, 1e-6, y=x, residual=x, residual_out=x, codes=x, scales=x, gs=x)
+    assert sys.getrefcount(x) == before
