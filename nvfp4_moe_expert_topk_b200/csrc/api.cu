@@ -56,6 +56,22 @@ int device_check(int *num_sms)
     return NVFP4_OK;
 }
 
+// cuTensorMapEncodeTiled needs a current context, which a host thread has only
+// after its first runtime call that works on the device.  In a thread without
+// one, the current device's primary context is made current and the call
+// repeated; any other thread's context stays as it is.
+template <typename... A>
+CUresult encode_tiled(A... args)
+{
+    CUresult r = g_encode(args...);
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+            r = g_encode(args...);
+    }
+    return r;
+}
+
 // 2-D uint8 tensor map over a row-major code matrix [rows, cols_bytes]
 // (row stride cols_bytes), box box_rows rows x 128 bytes, 128-byte swizzle;
 // rows and columns outside the matrix read as zero.
@@ -65,7 +81,7 @@ int make_code_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols_bytes)};
     cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+    CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
@@ -79,7 +95,7 @@ int make_out_map(CUtensorMap *map, void *base, int64_t rows, int64_t cols, int64
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldo * 2)};
     cuuint32_t box[2] = {32, 32};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+    CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
@@ -453,7 +469,7 @@ int nvfp4::byte_map(CUtensorMap *map, const void *base, int rank, const uint64_t
         if (i > 0)
             st[i - 1] = strides[i - 1];
     }
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+    const CUresult r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
                                 const_cast<void *>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -209,3 +209,152 @@ def test_balance_past_32_bits():
     assert int(c[0, 0]) == T - n
     assert torch.allclose(p[1], p2[0], rtol=1e-5) and torch.allclose(loss[1], loss2[0], rtol=1e-5)
     assert torch.equal(grad[-n:], grad2)                 # a row's gradient does not depend on the batch around it
+
+
+@pytest.mark.parametrize("make,args", CALLS)
+def test_threads_at_once(make, args):
+    """Four threads, each with its own data and stream (the interpreter lock
+    is not held while a call launches)."""
+    import threading
+
+    calls = [make(*args, seed) for seed in range(4)]
+    alone = []
+    for out, call in calls:
+        call()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in out])
+        for t in out:
+            t.zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(call, stream):
+        try:
+            for _ in range(50):
+                call(stream)
+        except Exception as e:          # reported by the test's own thread
+            errors.append(e)
+
+    streams = [torch.cuda.Stream() for _ in calls]
+    threads = [threading.Thread(target=work, args=(call, s)) for (_, call), s in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for (out, _), want in zip(calls, alone):
+        for a, b in zip(out, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_current_stream_is_used():
+    """Without a stream argument the call goes to the current stream."""
+    out, call = norm_call(300, 1536, 9)
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):     # a launch on another stream would not be recorded
+        call()
+    for t in out:
+        t.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_wrong_kinds_of_arguments():
+    x = torch.zeros(2, 256, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(TypeError):
+        lib.nvfp4_add_rmsnorm(x, w, "small", y=x)
+    with pytest.raises(TypeError):
+        lib.nvfp4_add_rmsnorm(x, w, 1e-6, y=x, quant="nvfp4")
+    with pytest.raises(AttributeError):
+        lib.nvfp4_add_rmsnorm(x, w, 1e-6, y=x, stream=7)
+    with pytest.raises(ValueError, match="x must be .T, H., got .256."):
+        lib.nvfp4_add_rmsnorm(w, w, 1e-6, y=x)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        lib.nvfp4_add_rmsnorm(x, w, 1e-6, y=x.to_sparse())
+    codes = torch.zeros(64, 128, dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(128 * 16, dtype=torch.uint8, device=DEV)
+    gs, out = torch.ones(1, device=DEV), torch.empty(2, 64, dtype=torch.bfloat16, device=DEV)
+    for seg in (64, None, ["a"], [1.5]):
+        with pytest.raises(TypeError):
+            lib.nvfp4_gemv(x, codes, scales, gs, seg, out)
+    with pytest.raises(lib.Nvfp4Error) as e:
+        lib.nvfp4_gemv(x, codes, scales, torch.ones(5, device=DEV), [1, 2, 3, 4, 64], out)
+    assert e.value.status == -2
+    for seg in ((64,), torch.tensor([64])):
+        lib.nvfp4_gemv(x, codes, scales, gs, seg, out)
+    l = torch.zeros(8, 16, device=DEV)
+    ids = torch.zeros(8, 2, dtype=torch.int32, device=DEV)
+    c, t = torch.zeros(1, 16, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    p, s = torch.zeros(1, 16, device=DEV), torch.zeros(1, device=DEV)
+    ws = torch.empty(lib.nvfp4_moe_balance_workspace_size(8, 1, 16), dtype=torch.uint8, device=DEV)
+    for k in (None, "2", 2.0):
+        with pytest.raises(TypeError):
+            lib.nvfp4_moe_balance(l, ids, k, c, t, p, s, ws)
+    with pytest.raises(ValueError, match="out of range"):
+        lib.nvfp4_moe_balance(l, ids, 2, c, t, p, s, ws, scoring=1 << 40)
+    for n in (0, 1):
+        with pytest.raises(ValueError, match="seq_offsets must hold"):
+            lib.nvfp4_moe_balance(l, ids, 2, c, t, p, s, ws, seq_offsets=t[:n])
+    with pytest.raises(lib.Nvfp4Error) as e:
+        lib.nvfp4_moe_balance(l, ids, 0, c, t, p, s, ws)
+    assert e.value.status == -1
+    lib.nvfp4_moe_balance(l, ids, 2, c, t, p, s, ws)
+
+
+def in_new_thread(call):
+    import threading
+
+    errors = []
+
+    def work():
+        try:
+            call()
+        except Exception as e:
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+
+
+@pytest.mark.parametrize("make,args", CALLS)
+def test_first_call_of_a_thread(make, args):
+    out, call = make(*args, 3)
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in out]
+    for t in out:
+        t.zero_()
+    in_new_thread(call)
+    for a, b in zip(out, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_first_call_of_a_thread_dense_gemm():
+    """The dense product builds tensor maps before its first launch, like the
+    few-row one."""
+    M, N, K = 130, 256, 512
+    g = torch.Generator(device=DEV).manual_seed(1)
+
+    def operand(rows):
+        codes = torch.randint(0, 256, (rows, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+        scales = torch.randint(8, 100, (lib.nvfp4_scales_bytes(rows, K, lib.NVFP4_SCALES_MMA),), generator=g, device=DEV,
+                               dtype=torch.uint8)
+        return codes, scales, torch.ones(1, device=DEV)
+
+    a, b = operand(M), operand(N)
+    want, out = (torch.zeros(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    lib.nvfp4_gemm(*a, *b, [N], want)
+    in_new_thread(lambda: lib.nvfp4_gemm(*a, *b, [N], out))
+    assert want.abs().sum() > 0 and torch.equal(bits(out), bits(want))
