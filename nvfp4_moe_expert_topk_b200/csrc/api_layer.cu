@@ -19,10 +19,9 @@ int status_of(cudaError_t e)
 }
 
 // Workspace of nvfp4_moe_balance: per chunk slot E probability sums and E
-// counts (padded to 4) and the token count; per sequence the loss's parts and
-// a counter.
+// counts (padded to 4) and the token count.
 struct BalanceLayout {
-    int64_t part_c, part_dot, part_n, done, total;
+    int64_t part_c, part_n, total;
 };
 
 BalanceLayout balance_layout(int64_t T, int64_t S, int64_t E)
@@ -30,10 +29,8 @@ BalanceLayout balance_layout(int64_t T, int64_t S, int64_t E)
     BalanceLayout L;
     const int64_t slots = balance_slots(T, S, static_cast<int>(E)), row = (E + 3) / 4 * 16;
     L.part_c = slots * row;
-    L.part_dot = 2 * L.part_c;
-    L.part_n = L.part_dot + S * balance_sum_blocks(static_cast<int>(E)) * 8;
-    L.done = L.part_n + 4 * slots;
-    L.total = L.done + 4 * S;
+    L.part_n = 2 * L.part_c;
+    L.total = L.part_n + 4 * slots;
     return L;
 }
 
@@ -206,8 +203,6 @@ int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_i
     a.part_p = reinterpret_cast<float *>(ws);
     a.part_c = reinterpret_cast<int32_t *>(ws + L.part_c);
     a.part_n = reinterpret_cast<int32_t *>(ws + L.part_n);
-    a.part_dot = reinterpret_cast<double *>(ws + L.part_dot);
-    a.done = reinterpret_cast<int32_t *>(ws + L.done);
     return status_of(launch_balance(a, static_cast<cudaStream_t>(stream)));
 }
 

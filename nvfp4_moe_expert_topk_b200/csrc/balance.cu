@@ -25,16 +25,16 @@
 // token's row, ids and weight gradients are loaded while the current one is
 // worked on.
 #include "internal.h"
+#include "ptx.cuh"
 #include "quant.cuh"
 
 namespace nvfp4 {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;                   // block of the gradient
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWholeThreads = 512;          // block of the one-launch form for short batches
-constexpr int kWholeTokens = 512;           // the longest batch it takes
+constexpr int kSumThreads = 512;            // block that adds chunks up
 constexpr unsigned kAll = 0xffffffffu;
 
 // Columns of a chunk's row of sums, so that rows start on 16 bytes.
@@ -71,6 +71,18 @@ __device__ __forceinline__ float warp_max(float v)
     float m;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
+}
+
+// All threads of the cluster; what was stored before an arrival is seen after
+// the wait.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // exp(x), x <= 0 or moderate: 2^(x log2 e) on the special-function unit, off by
@@ -207,20 +219,21 @@ __device__ __forceinline__ float inverse(float x)
 __host__ __device__ constexpr int tokens_held(int P) { return P == 1 ? 4 : P <= 4 ? 2 : 1; }
 
 // Blocks per SM, by the registers that a row of up to 128 P columns takes.
-__host__ __device__ constexpr int chunk_blocks(int P) { return P <= 3 ? 4 : P <= 4 ? 3 : 2; }
+// (Few blocks of many warps: half as many chunks to add up as with eight warps each.)
+__host__ __device__ constexpr int chunk_warps(int P, bool whole) { return P == 4 && !whole ? 12 : 16; }
+__host__ __device__ constexpr int chunk_blocks(int P) { return P <= 4 ? 2 : 1; }
 __host__ __device__ constexpr int backward_blocks(int P) { return P <= 2 ? 4 : P == 4 ? 2 : 3; }
 
 // Sums of a run of tokens of one sequence: a chunk's, left in the workspace, or
 // (WHOLE, short batches) a whole sequence's, with its loss, in one launch.
 template <int P, bool V4, bool SIG, bool WHOLE>
-__global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : chunk_blocks(P)) balance_chunk_kernel(const BalanceArgs a)
+__global__ void __launch_bounds__(32 * chunk_warps(P, WHOLE), WHOLE ? 1 : chunk_blocks(P)) balance_chunk_kernel(const BalanceArgs a)
 {
-    constexpr int W = (WHOLE ? kWholeThreads : kThreads) / 32, D = tokens_held(P);
+    constexpr int W = chunk_warps(P, WHOLE), D = tokens_held(P);
     extern __shared__ float sm[];                 // [W][E] probability sums, then [E] int counts
     __shared__ int tokens_s;
     __shared__ double red[W];
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, slot = blockIdx.x;
     int seq, t0, t1;
@@ -293,6 +306,7 @@ __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : 
             sm[warp * E + c] = acc[q];
     }
     __syncthreads();
+    pdl_trigger();                                 // (the next kernel's blocks would only be in the way before)
     const int Ep = padded(E);
     double dot = 0.0;
     for (int e = threadIdx.x; e < E; e += 32 * W) {
@@ -325,70 +339,96 @@ __global__ void __launch_bounds__(WHOLE ? kWholeThreads : kThreads, WHOLE ? 1 : 
         }
     } else if (threadIdx.x == 0) {
         a.part_n[slot] = tokens_s;
-        if (slot == first_slot(a, seq))
-            a.done[seq] = 0;                       // the second kernel's blocks of this sequence count themselves
     }
 }
 
-// Sums over a sequence's chunks: block (x, s) does kCols experts of sequence s,
-// thread (c, i) four of them in the chunks i, i + kRows, ...; the sums of the
-// kRows threads are added in order.  The loss is the sum of the blocks' parts
-// in block order, by the block that finds all others done.
-constexpr int kCols = 32, kRows = kThreads / (kCols / 4);
+// Sums over a sequence's chunks and its loss: one cluster of blocks per
+// sequence, block x for the experts [x, x + 1) * cols; one half of its threads
+// adds probabilities, the other counts, thread (i, c) four experts' in the
+// chunks i, i + rows, ...; the rows' sums and the blocks' parts of the loss
+// (through shared memory of the cluster's first block) are added in order.
+// Bound by latency: the offsets, then up to kSumLoads loads of a thread at once
+// (four arrays' worth of half as many took 0.5 to 3 us more), then two
+// meetings.
+constexpr int kSumLoads = 8;
+constexpr int kSumRows = 32;                       // at most
 
-__global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalanceArgs a)
+__global__ void __launch_bounds__(kSumThreads, 2) balance_sum_kernel(const BalanceArgs a, int cols)
 {
-    __shared__ double sp[kRows][kCols + 1];
-    __shared__ int sc[kRows][kCols + 1];
-    __shared__ int sn[kThreads / 32];
-    __shared__ int last_s;
+    constexpr int kHalf = kSumThreads / 2;
+    __shared__ double sp[4 * kHalf];
+    __shared__ int sc[4 * kHalf];
+    __shared__ int sn[kSumThreads / 32];
+    __shared__ double red[kSumThreads / 32], dots[8];
+    const int blocks = gridDim.x, rank = blockIdx.x;
+    if (blocks > 1)
+        cluster_arrive();                          // waited for before the store to the first block
+    const int quads = cols / 4, rows = min(kHalf / quads, kSumRows);
+    const int half = threadIdx.x % kHalf, row = half / quads, c4 = 4 * (half - row * quads);
+    const int s = blockIdx.y, E = a.E, Ep = padded(E), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    pdl_trigger();
-    const int s = blockIdx.y, E = a.E, Ep = padded(E);
     const int o0 = seq_start(a, s), o1 = seq_start(a, s + 1);
-    const int slot0 = first_slot(a, s);
+    const int slot0 = o0 / a.chunk + s;
     const int nslots = o1 > o0 ? (o1 - 1) / a.chunk - o0 / a.chunk + 1 : 0;    // non-empty ones
-    const int c4 = 4 * (threadIdx.x % (kCols / 4)), row = threadIdx.x / (kCols / 4);
-    const int e0 = blockIdx.x * kCols + c4;
-    double p[4] = {0.0, 0.0, 0.0, 0.0};
-    int c[4] = {0, 0, 0, 0};
-    if (e0 < E) {
-        const float *pp = a.part_p + static_cast<int64_t>(slot0) * Ep + e0;
-        const int32_t *pc = a.part_c + static_cast<int64_t>(slot0) * Ep + e0;
-#pragma unroll 4
-        for (int i = row; i < nslots; i += kRows) {
-            const float4 f = __ldcg(reinterpret_cast<const float4 *>(pp + static_cast<int64_t>(i) * Ep));
-            const int4 n = __ldcg(reinterpret_cast<const int4 *>(pc + static_cast<int64_t>(i) * Ep));
-            p[0] += f.x, p[1] += f.y, p[2] += f.z, p[3] += f.w;
-            c[0] += n.x, c[1] += n.y, c[2] += n.z, c[3] += n.w;
-        }
-    }
     int n = 0;
-    for (int i = threadIdx.x; i < nslots; i += kThreads)
+    for (int i = threadIdx.x; i < nslots; i += kSumThreads)
         n += __ldcg(a.part_n + slot0 + i);
-    n = __reduce_add_sync(kAll, n);
-    if ((threadIdx.x & 31) == 0)
-        sn[threadIdx.x >> 5] = n;
+    const bool mine = row < rows && rank * cols + c4 < E;
+    const int64_t first = static_cast<int64_t>(slot0) * Ep + rank * cols + c4;
+    const int at = row * cols + c4;
+    if (threadIdx.x < kHalf) {
+        double p[4] = {0.0, 0.0, 0.0, 0.0};
+        for (int i = row; mine && i < nslots; i += kSumLoads * rows) {
+            float4 f[kSumLoads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        sp[row][c4 + j] = p[j];
-        sc[row][c4 + j] = c[j];
+            for (int u = 0; u < kSumLoads; ++u)
+                f[u] = i + u * rows < nslots ? __ldcg(reinterpret_cast<const float4 *>(
+                                                   a.part_p + first + static_cast<int64_t>(i + u * rows) * Ep))
+                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int u = 0; u < kSumLoads; ++u)
+                p[0] += f[u].x, p[1] += f[u].y, p[2] += f[u].z, p[3] += f[u].w;
+        }
+        if (row < rows)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sp[at + j] = p[j];
+    } else {
+        int c[4] = {0, 0, 0, 0};
+        for (int i = row; mine && i < nslots; i += kSumLoads * rows) {
+            int4 m[kSumLoads];
+#pragma unroll
+            for (int u = 0; u < kSumLoads; ++u)
+                m[u] = i + u * rows < nslots ? __ldcg(reinterpret_cast<const int4 *>(
+                                                   a.part_c + first + static_cast<int64_t>(i + u * rows) * Ep))
+                                             : make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < kSumLoads; ++u)
+                c[0] += m[u].x, c[1] += m[u].y, c[2] += m[u].z, c[3] += m[u].w;
+        }
+        if (row < rows)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sc[at + j] = c[j];
     }
+    pdl_trigger();
+    n = __reduce_add_sync(kAll, n);
+    if (lane == 0)
+        sn[warp] = n;
     __syncthreads();
-    if (threadIdx.x >= 32)
-        return;
     n = 0;
-    for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+    for (int w = 0; w < kSumThreads / 32; ++w)
         n += sn[w];
-    const int e = blockIdx.x * kCols + threadIdx.x;
+    const int e = rank * cols + threadIdx.x;
     double dot = 0.0;
-    if (e < E) {
+    if (threadIdx.x < cols && e < E) {
         double ps = 0.0;
         int cs = 0;
 #pragma unroll 8
-        for (int i = 0; i < kRows; ++i) {
-            ps += sp[i][threadIdx.x];
-            cs += sc[i][threadIdx.x];
+        for (int i = 0; i < rows; ++i) {
+            ps += sp[i * cols + threadIdx.x];
+            cs += sc[i * cols + threadIdx.x];
         }
         a.counts[static_cast<int64_t>(s) * E + e] = cs;
         a.probs[static_cast<int64_t>(s) * E + e] = static_cast<float>(ps);
@@ -397,38 +437,39 @@ __global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalanceArgs
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         dot += __shfl_xor_sync(kAll, dot, o);
-    if (threadIdx.x != 0)
-        return;
-    if (blockIdx.x == 0)
-        a.tokens[s] = n;
-    const int blocks = gridDim.x;
-    if (n == 0) {
-        if (blockIdx.x == 0)
-            a.loss[s] = 0.0f;
-        return;
+    if (lane == 0)
+        red[warp] = dot;
+    __syncthreads();
+    if (blocks > 1)
+        cluster_wait();
+    if (threadIdx.x == 0) {
+        dot = 0.0;
+        for (int w = 0; w < kSumThreads / 32; ++w)
+            dot += red[w];
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(map_shared_to_cta(smem_u32(dots + rank), 0)), "d"(dot)
+                     : "memory");
     }
     if (blocks > 1) {
-        // (a sequence with tokens has chunks, so its counter was set to 0)
-        a.part_dot[static_cast<int64_t>(s) * blocks + blockIdx.x] = dot;
-        __threadfence();
-        last_s = atomicAdd(a.done + s, 1) == blocks - 1;
-        if (!last_s)
-            return;
-        __threadfence();
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (rank == 0 && threadIdx.x == 0) {
         dot = 0.0;
         for (int i = 0; i < blocks; ++i)
-            dot += __ldcg(a.part_dot + static_cast<int64_t>(s) * blocks + i);
+            dot += dots[i];
+        a.tokens[s] = n;
+        a.loss[s] = n == 0 ? 0.0f : static_cast<float>(dot * E / (static_cast<double>(a.k) * n * n));
     }
-    a.loss[s] = static_cast<float>(dot * E / (static_cast<double>(a.k) * n * n));
 }
 
-// Gradient: one warp per token, consecutive tokens per warp.
+// Gradient: one warp per token, consecutive tokens per warp.  The next kernel's
+// blocks come when this one's leave: they would take issue slots for nothing
+// (4096 x 384: 5.5 us, 6.4 with an early trigger).
 template <int P, bool V4, bool SIG>
 __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward_kernel(const BalanceArgs a, int per_warp)
 {
     extern __shared__ __align__(16) float sm[];   // [kWarps][E]: the weights' part of a row
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E;
     float *extra = sm + warp * E;
@@ -593,18 +634,16 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
 
 // Tokens per chunk: about as many chunks as blocks fit on the 148 SMs of the
 // device (more, shorter ones pay each block's start and end; fewer leave SMs
-// idle), but a token per warp at least.
+// idle), but a token per warp at least, and two where one would leave more
+// chunks of a sequence than its second kernel reads at once (4096 x 384: one
+// sequence 6.7 us with two and 8.2 with one, seven sequences 8.3 and 7.6).
 int balance_chunk(int64_t T, int64_t S, int E)
 {
-    const int64_t fit = 148 * chunk_blocks((E + 127) / 128);
+    const int P = (E + 127) / 128;
+    const int64_t fit = 148 * chunk_blocks(P), warps = chunk_warps(P, false);
     const int64_t blocks = S < fit / 2 ? fit - S : fit / 2;    // (every sequence may add a chunk)
-    const int64_t c = (T + blocks - 1) / blocks;
-    return static_cast<int>(c < kWarps ? kWarps : c);
-}
-
-int balance_sum_blocks(int E)
-{
-    return (E + kCols - 1) / kCols;
+    const int64_t c = (T + blocks - 1) / blocks, least = T > 128 * warps * S ? 2 * warps : warps;
+    return static_cast<int>(c < least ? least : c);
 }
 
 int64_t balance_slots(int64_t T, int64_t S, int E)
@@ -630,24 +669,18 @@ static bool aligned_rows(const BalanceArgs &a)
 
 namespace {
 
-template <int P, bool V4, bool SIG>
+template <int P, bool V4, bool SIG, bool WHOLE>
 cudaError_t chunk_launch(const BalanceArgs &a, cudaStream_t s)
 {
-    return launch_pdl(balance_chunk_kernel<P, V4, SIG, false>, dim3(static_cast<unsigned>(balance_slots(a.T, a.S, a.E))),
-                      dim3(kThreads), sizeof(float) * (kWarps + 1) * a.E, s, a);
-}
-
-template <int P, bool V4, bool SIG>
-cudaError_t whole_launch(const BalanceArgs &a, cudaStream_t s)
-{
+    const int64_t blocks = WHOLE ? a.S : balance_slots(a.T, a.S, a.E);
     static unsigned long long attr_done = 0;
-    constexpr int W = kWholeThreads / 32;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(balance_chunk_kernel<P, V4, SIG, true>),
-                                            sizeof(float) * (W + 1) * 1024, &attr_done);
+    constexpr int W = chunk_warps(P, WHOLE);
+    const auto kernel = balance_chunk_kernel<P, V4, SIG, WHOLE>;
+    const cudaError_t e =
+        ensure_smem_limit(reinterpret_cast<const void *>(kernel), sizeof(float) * (W + 1) * 128 * P, &attr_done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(balance_chunk_kernel<P, V4, SIG, true>, dim3(static_cast<unsigned>(a.S)), dim3(kWholeThreads),
-                      sizeof(float) * (W + 1) * a.E, s, a);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * W), sizeof(float) * (W + 1) * a.E, s, a);
 }
 
 template <int P, bool V4, bool SIG>
@@ -663,14 +696,14 @@ cudaError_t backward_launch(const BalanceArgs &a, cudaStream_t s)
 
 cudaError_t launch_chunks(const BalanceArgs &a, cudaStream_t s)
 {
-#define F(P, V, S) chunk_launch<P, V, S>(a, s)
+#define F(P, V, S) chunk_launch<P, V, S, false>(a, s)
     NVFP4_BALANCE_CASES(F)
 #undef F
 }
 
 cudaError_t launch_whole(const BalanceArgs &a, cudaStream_t s)
 {
-#define F(P, V, S) whole_launch<P, V, S>(a, s)
+#define F(P, V, S) chunk_launch<P, V, S, true>(a, s)
     NVFP4_BALANCE_CASES(F)
 #undef F
 }
@@ -679,14 +712,32 @@ cudaError_t launch_whole(const BalanceArgs &a, cudaStream_t s)
 
 cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t s)
 {
-    if (a.T <= kWholeTokens)
+    // One launch for short batches, a block per sequence.  With all tokens in one
+    // sequence it takes as long as two launches at 190 tokens of 48 or 128
+    // experts, 160 of 256, 150 of 384, 128 of 512 and 95 of 1024 (6 to 8 us;
+    // 64 x 48: 3.3 us instead of 5.8; 512 x 512: 19.2 instead of 6.9).
+    if (a.T * (a.E + 700) <= 128 * (512 + 700))
         return launch_whole(a, s);
     const cudaError_t e = launch_chunks(a, s);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(balance_sum_kernel,
-                      dim3(static_cast<unsigned>(balance_sum_blocks(a.E)), static_cast<unsigned>(a.S)), dim3(kThreads),
-                      0, s, a);
+    // up to 8 blocks per sequence, 32 experts each at least
+    const int blocks = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : 8;
+    const int cols = padded((a.E + blocks - 1) / blocks);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.S));
+    cfg.blockDim = dim3(kSumThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, balance_sum_kernel, a, cols);
 }
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, cudaStream_t s)

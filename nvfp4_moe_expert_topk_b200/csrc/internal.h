@@ -239,14 +239,11 @@ struct BalanceArgs {
     float *probs, *loss;
     float *part_p;            // per chunk slot: sums and counts (rows padded to 4 columns), tokens
     int32_t *part_c, *part_n;
-    double *part_dot;         // per sequence and block of the second kernel: its part of the loss
-    int32_t *done;            // per sequence: such blocks that are done
     const float *grad_loss, *grad_weights;
     float *grad_logits;
 };
 int balance_chunk(int64_t T, int64_t S, int E);
 int64_t balance_slots(int64_t T, int64_t S, int E);
-int balance_sum_blocks(int E);
 cudaError_t launch_balance(const BalanceArgs &args, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs &args, cudaStream_t s);
 
