@@ -267,6 +267,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     __syncwarp();
     pdl_wait();
     pdl_trigger();
+    // the largest exponent of each row's piece of k; the first pieces stay in
+    // registers until they are converted.  (Their loads go out before the
+    // weights', which would keep them waiting.)
+    uint4 keep[MT][kKeep];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u)
+            keep[m][u] = warp + u * warps < (b1 - b0) * 8 ? piece(m, b0, warp + u * warps) : make_uint4(0, 0, 0, 0);
+    asm volatile("" ::: "memory");
     if (whole) {
         share(b0, b1 - b0);
         f_end = pl.rounds;
@@ -275,14 +285,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     }
     if (threadIdx.x < a.nseg)
         inv_gs[threadIdx.x] = __fdiv_rn(1.0f, __ldg(a.gs + threadIdx.x));
-    // the largest exponent of each row's piece of k; the first pieces stay in
-    // registers until they are converted
-    uint4 keep[MT][kKeep];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int u = 0; u < kKeep; ++u)
-            keep[m][u] = warp + u * warps < (b1 - b0) * 8 ? piece(m, b0, warp + u * warps) : make_uint4(0, 0, 0, 0);
     __syncthreads();                               // expo is initialised
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -467,21 +469,37 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
             }
             dst = map_shared_to_cta(smem_u32(dst_own), it % cluster);
         }
-#pragma unroll
-        for (int v = 0; v < kVals; ++v) {
-            if (pl.slices > 1 && v % pl.slices != slice)
-                continue;
-            float s = acc[v / (4 * MT)][v / 4 % MT][0][v & 3];
-            if (pl.slices > 1) {
-                s = red[v * 32];
-                for (int k = 1; k < pl.slices; ++k)
-                    s += red[(k * kVals + v) * 32];
-            }
+        auto pass_on = [&](int v, float s) {
             s = unscale(v, s);
             if (cluster > 1)
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + 128 * v), "f"(s) : "memory");
             else
                 store(tile, v, s);
+        };
+        if (pl.slices == 1) {
+#pragma unroll
+            for (int v = 0; v < kVals; ++v)
+                pass_on(v, acc[v / (4 * MT)][v / 4 % MT][0][v & 3]);
+        } else {
+            // two values at a time, all loads first, then the sums in order
+            for (int v = slice; v < kVals; v += 2 * pl.slices) {
+                const int w = v + pl.slices;
+                const float *r0 = red + v * 32, *r1 = red + (w < kVals ? w : v) * 32;
+                float p0[kMaxWarps], p1[kMaxWarps];
+#pragma unroll
+                for (int k = 0; k < kMaxWarps; ++k) {
+                    p0[k] = k < pl.slices ? r0[k * (kVals * 32)] : 0.0f;
+                    p1[k] = k < pl.slices ? r1[k * (kVals * 32)] : 0.0f;
+                }
+#pragma unroll
+                for (int k = 1; k < kMaxWarps; ++k) {
+                    p0[0] += p0[k];
+                    p1[0] += p1[k];
+                }
+                pass_on(v, p0[0]);
+                if (w < kVals)
+                    pass_on(w, p1[0]);
+            }
         }
     }
     if (!ok && lane == 0)                          // copies still in flight have landed before the block ends
@@ -496,10 +514,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         for (int it = rank; it < pl.rounds; it += cluster)
             for (int v = slice; v < kVals; v += pl.slices) {
                 const float *p = sums + ((it / cluster) * pl.groups + group) * (kVals * 32) + v * 32 + lane;
-                float s = 0.0f;
-                for (int r = 0; r < cluster; ++r)
-                    s += p[r * pl.owned() * pl.groups * (kVals * 32)];
-                store(tile_of(it), v, s);
+                const int ld = pl.owned() * pl.groups * (kVals * 32);
+                float part[8];                     // (a cluster has 8 blocks at most)
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    part[r] = r < cluster ? p[r * ld] : 0.0f;
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    part[0] += part[r];
+                store(tile_of(it), v, part[0]);
             }
     }
 }
