@@ -593,12 +593,12 @@ static GemvPlan complete_plan(const GemvArgs &a, int groups, int slices, int clu
     return p;
 }
 
-// Estimated time of a plan in 10 ns.  The weights of the terms are a fit to the
-// device times of all splits of 20 shapes (M 1 to 16, N 33 to 65536, K 64 to
-// 16384; off by 10 % rms, and the split it picks within 3 % of the best one
-// tried for most of them, 15 % at worst): a round's steps cost a latency and a
-// share per warp (decoding is bound by issue slots), plus the meeting of the
-// slices, the block's pieces of x per warp, and the meeting of the cluster.
+// Estimated time of a plan in 10 ns, less what all plans share.  The weights of
+// the terms are a fit to the device times of all splits of 22 shapes (M 1 to
+// 16, N 33 to 65536, K 64 to 16384; off by 10 % rms, and the split it picks
+// within 3 % of the best one tried for 17 of them, 13 % at worst): a round's
+// steps cost a latency and a share per warp, plus the meeting of the slices,
+// the block's pieces of x per warp, and the meeting of the cluster.
 static int plan_cost(const GemvPlan &p, int mt, int steps)
 {
     const int block_steps = (steps + p.cluster - 1) / p.cluster;
@@ -607,8 +607,8 @@ static int plan_cost(const GemvPlan &p, int mt, int steps)
     const bool sl = p.slices > 1, cl = p.cluster > 1;
     if (p.panel < block_steps)                             // x converted again for every tile
         return (1 << 28) + p.rounds * block_steps;
-    return mt == 1 ? p.rounds * (s * (58 + 10 * w) + 41 * sl + 56 * cl + 58) + 20 * pieces + 145 * cl
-                   : p.rounds * (s * (79 + 14 * w) + 163 * sl + 219 * cl + 12) + 48 * pieces + 181 * cl;
+    return mt == 1 ? p.rounds * (s * (26 + 12 * w) + 5 * cl + 83) + 21 * pieces + 119 * cl
+                   : p.rounds * (s * (80 + 13 * w) + 53 * sl) + 26 * pieces + 232 * cl;
 }
 
 template <int MT>
