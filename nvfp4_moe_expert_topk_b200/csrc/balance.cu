@@ -24,6 +24,13 @@
 // short ones: one warp per token with the row in registers, and the next
 // token's row, ids and weight gradients are loaded while the current one is
 // worked on.
+//
+// Measured (one B200, calls back to back): loss of 64 x 48 3.3 us, of 4096 x 384
+// in 7 sequences 7.7 us, of 65536 x 384 24.8 us (4.1 TB/s); gradient with weight
+// gradients of 4096 x 384 5.5 us, of 65536 x 384 48 us (4.2 TB/s).  The long ones
+// execute 173 and 420 instructions a token and warp (scores, sums, the slots'
+// part of the gradient) at 56 % of the issue rate.  Rows of 64 experts or fewer
+// leave half the lanes idle: 65536 x 48 takes 13.4 us and 27 us.
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"

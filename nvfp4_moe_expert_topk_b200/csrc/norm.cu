@@ -21,13 +21,18 @@
 // as fp32 addition and rounding to bf16 do (fp32 keeps 16 bits below bf16, so
 // its own rounding never moves a sum onto or over a border), and the largest
 // magnitude of a block is the largest 15-bit pattern.
+//
+// Measured (one B200, calls back to back): 1 x 7168 with residual and NVFP4
+// rows 2.9 us, 64 x 7168 to E4M3 3.1 us, 2041 x 1536 to NVFP4 4.6 us, 4096 x
+// 7168 with residual and NVFP4 rows 43.6 us = 5.8 TB/s, 88 % of a plain copy.
+// (One block per SM that loads its next row ahead was slower: 41 us against 27
+// without the residual.)
 #include "internal.h"
 #include "quant.cuh"
 
 namespace nvfp4 {
 
 namespace {
-
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float *f)
 {
