@@ -27,10 +27,10 @@
 //
 // Measured (one B200, calls back to back): loss of 64 x 48 3.3 us, of 4096 x 384
 // in 7 sequences 7.7 us, of 65536 x 384 24.8 us (4.1 TB/s); gradient with weight
-// gradients of 4096 x 384 5.5 us, of 65536 x 384 48 us (4.2 TB/s).  The long ones
-// execute 173 and 420 instructions a token and warp (scores, sums, the slots'
+// gradients of 4096 x 384 5.4 us, of 65536 x 384 46 us (4.4 TB/s).  The long ones
+// execute 173 and 380 instructions a token and warp (scores, sums, the slots'
 // part of the gradient) at 56 % of the issue rate.  Rows of 64 experts or fewer
-// leave half the lanes idle: 65536 x 48 takes 13.4 us and 27 us.
+// leave half the lanes idle: 65536 x 48 takes 13.4 us and 24 us.
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -222,7 +222,7 @@ __device__ __forceinline__ float inverse(float x)
 // Tokens a warp holds at a time: one is worked on in place while the others are
 // on their way (short rows need several to fill the memory's latency; of the
 // longest rows one alone leaves registers for half as many warps more, which
-// runs the gradient at 24000 x 1024 in 66 us instead of 94).
+// runs the gradient at 24000 x 1024 in 64 us instead of about 90).
 __host__ __device__ constexpr int tokens_held(int P) { return P == 1 ? 4 : P <= 4 ? 2 : 1; }
 
 // Blocks per SM, by the registers that a row of up to 128 P columns takes.
@@ -471,15 +471,16 @@ __global__ void __launch_bounds__(kSumThreads, 2) balance_sum_kernel(const Balan
 
 // Gradient: one warp per token, consecutive tokens per warp.  The next kernel's
 // blocks come when this one's leave: they would take issue slots for nothing
-// (4096 x 384: 5.5 us, 6.4 with an early trigger).
+// (4096 x 384: 5.4 us, about 6.3 with an early trigger).
 template <int P, bool V4, bool SIG>
 __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward_kernel(const BalanceArgs a, int per_warp)
 {
-    extern __shared__ __align__(16) float sm[];   // [kWarps][E]: the weights' part of a row
+    extern __shared__ __align__(16) float sm[];   // [kWarps][E]: the weights' part of a row; [kWarps][E] bytes: slots
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E;
     float *extra = sm + warp * E;
+    uint8_t *slot_of = reinterpret_cast<uint8_t *>(sm + kWarps * E) + warp * E;
     for (int e = lane; e < E; e += 32)
         extra[e] = 0.0f;
     const int64_t tw = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * per_warp;
@@ -546,6 +547,8 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
         const bool on = s >= 0 && id >= 0 && id < E;
         // (from L1: the row has just been read)
         const float l = on && a.grad_weights != nullptr ? __ldg(a.logits + at + id) : 0.0f;
+        if (on && a.grad_weights != nullptr)
+            slot_of[id] = static_cast<uint8_t>(lane);      // of slots of one expert, one stays
         if (__any_sync(kAll, on)) {
             // the row's scores, and the selected slots' for the weights' part
             float sums[4];
@@ -582,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
                 const float q = inverse(sums[2]);
                 const float d = v * q * (g - sums[3] * q) * slope;
                 // into the row by way of shared memory; slots of one expert add up in slot order
-                bool twin = false;
-                for (int j = 0; j + 1 < a.k; ++j)
-                    twin |= __shfl_sync(kAll, id, j) == id && lane > j;
-                if (!__any_sync(kAll, twin && on)) {
+                // (found by the slots' numbers: comparing them by shuffles took 40 instructions more, 48.5 us
+                // instead of 46.3 at 65536 x 384)
+                __syncwarp();
+                if (!__any_sync(kAll, on && slot_of[id] != lane)) {
                     if (on)
                         extra[id] = d;
                 } else {
@@ -698,7 +701,7 @@ cudaError_t backward_launch(const BalanceArgs &a, cudaStream_t s)
     const int64_t per = (a.T + warps - 1) / warps;
     const int64_t grid = (a.T + kWarps * per - 1) / (kWarps * per);
     return launch_pdl(balance_backward_kernel<P, V4, SIG>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                      sizeof(float) * kWarps * a.E, s, a, static_cast<int>(per));
+                      (sizeof(float) + 1) * kWarps * a.E, s, a, static_cast<int>(per));
 }
 
 cudaError_t launch_chunks(const BalanceArgs &a, cudaStream_t s)
