@@ -445,7 +445,8 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
  * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
  * scratch: calls sharing one must not overlap on the device.
  * 1 <= k <= min(E, 32), E <= 1024, 1 <= S <= 65535, T >= 0 (T = 0: logits and
- * topk_ids may be NULL; zeros are written).  Two launches. */
+ * topk_ids may be NULL; zeros are written).  One launch for short
+ * batches, two otherwise. */
 size_t nvfp4_moe_balance_workspace_size(int64_t T, int64_t S, int E);
 int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_ids, int64_t T, int E, int k,
                       const int32_t *seq_offsets, int64_t S, int scoring,

@@ -5,6 +5,7 @@ tensors.
     python -m nvfp4_moe_expert_topk_b200.build [--force]
 """
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -44,7 +45,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
             if f.read() == built_for:
                 return BINDING
     base = os.path.dirname(os.path.abspath(torch.__file__))
-    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cuda = os.path.dirname(os.path.dirname(shutil.which(NVCC) or NVCC))
     includes = [os.path.join(base, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
                 os.path.join(ROOT, "include")]
     tmp = BINDING + ".tmp"

@@ -198,6 +198,40 @@ def test_sizes(T, E, k, scoring):
     Case(T, E, k, S=3, scoring=scoring, seed=T + E, pad=0.2).check()
 
 
+@pytest.mark.parametrize("T,E,k", [(t, E, k) for E, k in [(1, 1), (7, 3), (48, 6), (130, 6), (384, 6), (509, 8), (1024, 5)]
+                                   for t in (128 * 1212 // (E + 700), 128 * 1212 // (E + 700) + 1, 600, 1537, 2049)])
+def test_borders_between_forms(T, E, k):
+    """Batch lengths around those where the number of launches and the tokens
+    per chunk change; more sequences than tokens in one of them."""
+    for S, scoring in ((0, "softmax"), (2, "sigmoid"), (13, "softmax"), (700, "sigmoid")):
+        Case(T, E, k, S=S, scoring=scoring, seed=T + S, pad=0.1).check()
+
+
+@pytest.mark.parametrize("T,E", [(5000, 40), (5000, 513), (20000, 1022)])
+def test_sums_over_chunks_add_up(T, E):
+    """Logits of 0: every token adds 1 / E to every probability sum and the
+    counts are known, so the sums over chunks and their borders are seen
+    whole, for one sequence and for many of odd lengths."""
+    l = torch.zeros(T, E, device=DEV)
+    ids = (torch.arange(T, device=DEV)[:, None] * 3 + torch.arange(2, device=DEV)).remainder(E).to(torch.int32)
+    for S in (1, 7, 160):
+        off = (torch.arange(S + 1, dtype=torch.int64) * T // S).to(torch.int32)
+        counts, tokens = (torch.empty(*n, dtype=torch.int32, device=DEV) for n in ((S, E), (S,)))
+        probs, loss = torch.empty(S, E, device=DEV), torch.empty(S, device=DEV)
+        ws = torch.full((nvfp4_moe_balance_workspace_size(T, S, E),), 0xFF, dtype=torch.uint8, device=DEV)
+        nvfp4_moe_balance(l, ids, 2, counts, tokens, probs, loss, ws, seq_offsets=off.to(DEV))
+        n = off.diff()
+        assert torch.equal(tokens.cpu(), n)
+        host = ids.cpu()
+        want = torch.stack([torch.bincount(host[a:b].flatten(), minlength=E) for a, b in zip(off[:-1], off[1:])])
+        assert torch.equal(counts.cpu(), want.to(torch.int32))
+        # 1 / E rounded, then fp32 sums of at most T / 64 terms by a warp and of 16 warps, and the last rounding
+        bound = (T / 64 + 20) * 2.0 ** -24
+        P = n[:, None].double() / E
+        assert ((probs.cpu().double() - P).abs() <= bound * P).all()
+        assert ((loss.cpu().double() - 1).abs() <= 2 * bound).all()
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_long_batch(scoring):
     Case(20011, 384, 6, S=0, scoring=scoring, seed=3).check()
