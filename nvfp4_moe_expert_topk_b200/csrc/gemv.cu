@@ -14,11 +14,15 @@
 // two sets of 8) as its columns.  (mma.sync and not tcgen05: the operand is
 // made in registers, and at 8 or 16 columns the tensor pipe idles either way.)
 //
-// x in f16: each row's piece of k that a warp sums is scaled by a power of two
+// x in f16: each row's piece of k that a block sums is scaled by a power of two
 // that brings its largest magnitude into [2^14, 2^15); f16 then holds a bf16
-// value exactly down to 2^-31 of that largest one, and rounds what is smaller
-// to within 2^-39 of it -- 2^15 below the fp32 rounding of the largest
-// product.  The power of two is undone in fp32.
+// value exactly down to 2^-31 of that largest one.  The power of two is undone
+// in fp32.  A block one of whose rows holds a smaller value (not zero) works on
+// bf16 operands instead: x as it is, and the weights (6 significant bits) turned
+// from f16 to bf16 at three more instructions a pair.  Such a value may be all
+// that a sum consists of, if the large ones meet weights of zero.  So x is never
+// rounded, whatever it holds.  (Of normally distributed rows one launch in some
+// thousands has such a block.)
 //
 // Tiles.  A warp works on row tiles of 32 rows, 8 consecutive ones g in each
 // 32-row quarter of a 128-row scale block: the four rows' scales of 64 columns
@@ -48,6 +52,7 @@
 // did not shorten a step; a loop of half the code lengthened it by 3 %.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -91,6 +96,17 @@ __device__ __forceinline__ void scale_pairs(uint32_t v, uint32_t (&s)[2])
     s[1] = __byte_perm(h, 0u, 0x3232);
 }
 
+// f16 pair -> bf16 pair.
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t h)
+{
+    uint32_t d;
+    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 a, b;\n\tmov.b32 {lo, hi}, %1;\n\t"
+        "cvt.f32.f16 a, lo;\n\tcvt.f32.f16 b, hi;\n\tcvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+        : "=r"(d)
+        : "r"(h));
+    return d;
+}
+
 // bf16 pair times a power of two (both halves of p2) -> f16 pair.
 __device__ __forceinline__ uint32_t to_f16x2(uint32_t x, uint32_t p2)
 {
@@ -106,6 +122,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                                         uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -254,6 +279,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         xs[(i * pl.rows + 8 * m + g) * 4 + t] =
             make_uint4(to_f16x2(v.x, p2), to_f16x2(v.y, p2), to_f16x2(v.z, p2), to_f16x2(v.w, p2));
     };
+    // the same on bf16 operands: x as it is
+    auto copy = [&](int p0, int n) {
+        for (int m = 0; m < MT; ++m)
+            if (8 * m + g < a.M)
+                for (int i = warp; i < 8 * n; i += warps)
+                    xs[(i * pl.rows + 8 * m + g) * 4 + t] = piece(m, p0, i);
+    };
     // 2^(141 - exponent) in bf16, twice
     auto power = [&](int m) { return (268u - expo[8 * m + g]) * 0x00800080u; };
     auto convert = [&](int p0, int n, int from) {
@@ -295,12 +327,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     if (threadIdx.x < a.nseg)
         inv_gs[threadIdx.x] = __fdiv_rn(1.0f, __ldg(a.gs + threadIdx.x));
     __syncthreads();                               // expo is initialised
+    uint32_t low[MT];                              // the lane's smallest magnitude but 0, less 1
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        uint32_t mx = 0;
+        uint32_t mx = 0, mn = 0xFFFFFFFFu;
         auto top = [&](const uint4 &v) {
-            mx = __vmaxu2(mx, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
-            mx = __vmaxu2(mx, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+            const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mx = __vmaxu2(mx, w[i]);
+                mn = __viaddmin_u16x2(w[i], 0xFFFFFFFFu, mn);      // (0 becomes the largest)
+            }
         };
 #pragma unroll
         for (int u = 0; u < kKeep; ++u)
@@ -313,8 +350,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         mx = max(mx & 0xFFFFu, mx >> 16) >> 7;
         if (t == 0 && mx > 15u)
             atomicMax(&expo[8 * m + g], mx);
+        low[m] = min(mn & 0xFFFFu, mn >> 16);
     }
     __syncthreads();
+    // a value more than 31 binades below its row's largest (of a row that is finite)
+    int far = 0;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int e = static_cast<int>(expo[8 * m + g]);
+        far |= e < 255 && static_cast<int>(low[m]) + 1 < (e - 31) * 128;
+    }
     if (whole) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -323,6 +368,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
                 if (8 * m + g < a.M && warp + u * warps < (b1 - b0) * 8)
                     put(m, warp + u * warps, keep[m][u], power(m));
         convert(b0, b1 - b0, warp + kKeep * warps);
+    }
+    const bool wide = __syncthreads_or(far) != 0;  // bf16 operands
+    if (__builtin_expect(wide, 0)) {
+        if (threadIdx.x < 8 * MT)
+            expo[threadIdx.x] = 141u;              // nothing to undo
+        if (whole)
+            copy(b0, b1 - b0);
         __syncthreads();
     }
 
@@ -354,77 +406,98 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 #pragma unroll
                 for (int v = 0; v < 4 * kChains; ++v)
                     acc[p][m][v >> 2][v & 3] = 0.0f;
-        for (int p0 = b0; p0 < b1; p0 += pl.panel) {
-            if (!whole) {                          // x does not fit: panel by panel, again for every tile
-                const int n = min(pl.panel, b1 - p0);
-                __syncthreads();                   // the previous panel of x is read
-                convert(p0, n, warp);
-                __syncthreads();
-                share(p0, n);
-                f_it = it;
-                f_end = it + 1;
-                for (int d = 0; d < pl.depth; ++d)
-                    if (ok)
-                        fetch();
-            }
-            for (int step = first; step < last && ok; ++step) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &never_abort));
-                if (!ok)
-                    break;
-                const uint8_t *cs = codes_s + slot * kCodeStage + g * 128;
-                uint4 s4 = *reinterpret_cast<const uint4 *>(scales_s + slot * kScaleStage + t * 128 + g * 16);
-                if (step * kStep + 64 * t >= K)
-                    s4 = make_uint4(0, 0, 0, 0);   // scales past K are not loaded
-                const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
-                const uint4 *xp[MT];
+        // the tile's sums over this warp's steps, on f16 or on bf16 operands
+        auto sum_steps = [&](auto form) {
+            constexpr bool kWide = decltype(form)::value;
+            const auto mma = [](auto &...v) {
+                if (kWide)
+                    mma_bf16(v...);
+                else
+                    mma_f16(v...);
+            };
+            for (int p0 = b0; p0 < b1; p0 += pl.panel) {
+                if (!whole) {                          // x does not fit: panel by panel, again for every tile
+                    const int n = min(pl.panel, b1 - p0);
+                    __syncthreads();                   // the previous panel of x is read
+                    if (kWide)
+                        copy(p0, n);
+                    else
+                        convert(p0, n, warp);
+                    __syncthreads();
+                    share(p0, n);
+                    f_it = it;
+                    f_end = it + 1;
+                    for (int d = 0; d < pl.depth; ++d)
+                        if (ok)
+                            fetch();
+                }
+                for (int step = first; step < last && ok; ++step) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bar[slot], phase, &never_abort));
+                    if (!ok)
+                        break;
+                    const uint8_t *cs = codes_s + slot * kCodeStage + g * 128;
+                    uint4 s4 = *reinterpret_cast<const uint4 *>(scales_s + slot * kScaleStage + t * 128 + g * 16);
+                    if (step * kStep + 64 * t >= K)
+                        s4 = make_uint4(0, 0, 0, 0);   // scales past K are not loaded
+                    const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w};
+                    const uint4 *xp[MT];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)       // columns past M repeat row M - 1; their sums are not stored
-                    xp[m] = xs + ((step - p0) * 8 * pl.rows + min(8 * m + g, pl.rows - 1)) * 4 + t;
+                    for (int m = 0; m < MT; ++m)       // columns past M repeat row M - 1; their sums are not stored
+                        xp[m] = xs + ((step - p0) * 8 * pl.rows + min(8 * m + g, pl.rows - 1)) * 4 + t;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {      // 32 of the lane's 64 columns
-                    uint32_t sc[4][2];
-                    uint4 c[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        scale_pairs(h ? sw[j] >> 16 : sw[j], sc[j]);
-                        c[j] = *reinterpret_cast<const uint4 *>(cs + 1024 * j + (((2 * t + h) ^ g) << 4));
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // eight of them
-                        uint32_t v[4][4];
+                    for (int h = 0; h < 2; ++h) {      // 32 of the lane's 64 columns
+                        uint32_t sc[4][2];
+                        uint4 c[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            e2m1_pairs(q == 0 ? c[j].x : q == 1 ? c[j].y : q == 2 ? c[j].z : c[j].w, v[j]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[j][e] = mul_f16x2(v[j][e], sc[j][q >> 1]);
+                            scale_pairs(h ? sw[j] >> 16 : sw[j], sc[j]);
+                            c[j] = *reinterpret_cast<const uint4 *>(cs + 1024 * j + (((2 * t + h) ^ g) << 4));
                         }
-                        uint4 x[MT];
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            x[m] = xp[m][(4 * h + q) * 4 * pl.rows];
+                        for (int q = 0; q < 4; ++q) {  // eight of them
+                            uint32_t v[4][4];
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)                // rows 64 p and 64 p + 32 of the block
+                            for (int j = 0; j < 4; ++j) {
+                                e2m1_pairs(q == 0 ? c[j].x : q == 1 ? c[j].y : q == 2 ? c[j].z : c[j].w, v[j]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                {
+                                    v[j][e] = mul_f16x2(v[j][e], sc[j][q >> 1]);
+                                    if (kWide)
+                                        v[j][e] = to_bf16x2(v[j][e]);
+                                }
+                            }
+                            uint4 x[MT];
 #pragma unroll
                             for (int m = 0; m < MT; ++m)
-                                mma_f16(acc[p][m][0], v[2 * p][0], v[2 * p + 1][0], v[2 * p][1], v[2 * p + 1][1],
-                                        x[m].x, x[m].y);
+                                x[m] = xp[m][(4 * h + q) * 4 * pl.rows];
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
+                            for (int p = 0; p < 2; ++p)                // rows 64 p and 64 p + 32 of the block
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
-                                mma_f16(acc[p][m][kChains - 1], v[2 * p][2], v[2 * p + 1][2], v[2 * p][3],
-                                        v[2 * p + 1][3], x[m].z, x[m].w);
+                                for (int m = 0; m < MT; ++m)
+                                    mma(acc[p][m][0], v[2 * p][0], v[2 * p + 1][0], v[2 * p][1], v[2 * p + 1][1], x[m].x,
+                                        x[m].y);
+#pragma unroll
+                            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                                for (int m = 0; m < MT; ++m)
+                                    mma(acc[p][m][kChains - 1], v[2 * p][2], v[2 * p + 1][2], v[2 * p][3], v[2 * p + 1][3],
+                                        x[m].z, x[m].w);
+                        }
+                    }
+                    __syncwarp();                      // every lane has read the slot
+                    fetch();
+                    if (++slot == pl.depth) {
+                        slot = 0;
+                        phase ^= 1u;
                     }
                 }
-                __syncwarp();                      // every lane has read the slot
-                fetch();
-                if (++slot == pl.depth) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
             }
-        }
+        };
+        if (__builtin_expect(!wide, 1))
+            sum_steps(std::false_type{});
+        else
+            sum_steps(std::true_type{});
         if (kChains == 2)
 #pragma unroll
             for (int p = 0; p < 2; ++p)

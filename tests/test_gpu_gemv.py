@@ -237,3 +237,44 @@ def test_same_weights_as_the_dense_gemm():
     d, f = dense.double(), few.double()
     mag = x.double().abs() @ b.double().abs().t()
     assert ((d - f).abs() <= 2 * 2.0 ** -8 * d.abs() + 2 * (K / 8 + 33) * 2.0 ** -23 * 1.3 * mag).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 96, 64), (1, 2048, 7168), (3, 200, 256), (8, 130, 1984), (9, 33, 512), (16, 264, 448),
+                                   (5, 4100, 2048), (2, 70, 131072 + 64)])
+@pytest.mark.parametrize("top", [32, 45, 126])
+def test_large_values_on_zero_weights(M, N, K, top):
+    """Activations of 2^top whose weights are zero (by their code or by their
+    block's scale) beside ordinary ones and ones far below 1: what is left
+    of the sum comes from the small ones, so that the bound says whether they
+    were held."""
+    w = Weights(N, K, N + K)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).to(torch.bfloat16)
+    x[:, 16:32] *= 2.0 ** -30
+    big = [0, 1, 17, 40, K - 1, K - 20]
+    for i, c in enumerate(big):
+        x[i % M, c] = 2.0 ** top * (1 if i % 2 else -1)
+        w.codes[:, c // 2] &= 0x0F if c % 2 else 0xF0    # code 0 in the column
+    w.scales[:, 3] = 0                                   # and a whole block by its scale
+    x[M - 1, 48:52] = 2.0 ** top
+    w.codes[N // 2:, 16:] = 0                            # rows of only the smallest activations
+    check(M, N, K, w=w, x=x)
+
+
+@pytest.mark.parametrize("M", [1, 6, 16])
+def test_bands_of_magnitudes(M):
+    """Activations of very different magnitudes, each output made of one of
+    them alone: 2^-126 .. 2^100, subnormal ones beside them."""
+    N, K = 160, 640
+    w = Weights(N, K, 12)
+    keep = np.zeros((N, K), bool)
+    bands = np.arange(K) // 64                           # 10 bands of 64 columns
+    for n in range(N):
+        keep[n] = bands == n % 10
+    w.codes &= (np.where(keep[:, 0::2], 0x0F, 0) | np.where(keep[:, 1::2], 0xF0, 0)).astype(np.uint8)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).double()
+    p = np.array([100, 70, 37, 5, 0, -30, -61, -93, -110, -118])
+    x = (x * torch.from_numpy(2.0 ** p[bands])).to(torch.bfloat16)
+    got = check(M, N, K, w=w, x=x)
+    assert (np.abs(got[:, np.arange(N) % 10 < 9]).max(axis=1) > 0).all()
+    x[:, 64:] = 0.0                                      # one band alone, then the whole range in one row only
+    check(M, N, K, w=w, x=x)
