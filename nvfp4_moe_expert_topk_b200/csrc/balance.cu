@@ -115,6 +115,15 @@ __device__ __forceinline__ float sigmoid_fast(float x)
     return rcp_fast(1.0f + exp_fast(-x));
 }
 
+// sigmoid(x) and 1 - sigmoid(x) = sigmoid(-x), neither by subtraction: the smaller one is
+// e^-|x| / (1 + e^-|x|).
+__device__ __forceinline__ void sigmoid_pair(float x, float &s, float &complement)
+{
+    const float t = exp_fast(-fabsf(x)), large = rcp_fast(1.0f + t), small = t * large;
+    s = x < 0.0f ? small : large;
+    complement = x < 0.0f ? large : small;
+}
+
 // Start of sequence s (s = S: end of the last), clamped into [0, T].
 __device__ __forceinline__ int seq_start(const BalanceArgs &a, int s)
 {
@@ -552,19 +561,32 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
         if (__any_sync(kAll, on)) {
             // the row's scores, and the selected slots' for the weights' part
             float sums[4];
-            sums[0] = r.template scores<SIG>();
             sums[1] = 0.0f;
+            if (SIG) {
+                // in place: the smaller one of the score and its complement (their product is the slope)
+                sums[0] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4 * P; ++q)
-                sums[1] = fmaf(r.v[q], count(q), sums[1]);
+                for (int q = 0; q < 4 * P; ++q) {
+                    float sc, comp;
+                    sigmoid_pair(r.v[q], sc, comp);
+                    sums[0] += sc;
+                    sums[1] = fmaf(sc, count(q), sums[1]);
+                    r.v[q] = fminf(sc, comp);
+                }
+            } else {
+                sums[0] = r.template scores<false>();
+#pragma unroll
+                for (int q = 0; q < 4 * P; ++q)
+                    sums[1] = fmaf(r.v[q], count(q), sums[1]);
+            }
             float v = 0.0f, slope = 1.0f;
             if (a.grad_weights != nullptr) {
                 if (!SIG) {
                     const float m = warp_max(on ? l : -INFINITY);
                     v = on && m != -INFINITY ? exp_fast(l - m) : 0.0f;
                 } else {
-                    v = on ? sigmoid_fast(l) : 0.0f;
-                    slope = 1.0f - v;
+                    sigmoid_pair(l, v, slope);
+                    v = on ? v : 0.0f;
                 }
             }
             sums[2] = v;
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
                 const float sc = r.v[q];
                 r.v[q] = sc * fmaf(inv, count(q), dot);
                 if (SIG)
-                    r.v[q] *= 1.0f - sc;
+                    r.v[q] *= 1.0f - sc;           // (sc is 1/2 at most here: nothing cancels)
             }
             if (a.grad_weights != nullptr) {
                 // w (g - sum g w) with w = v / sum v

@@ -495,3 +495,54 @@ def test_refusals():
                           (dict(grad_weights=l), "grad_weights must hold"), (dict(grad_weights=ids), "grad_weights must be")]:
         with pytest.raises(ValueError, match=match):
             nvfp4_moe_balance_backward(**dict(back, **change))
+
+
+def sigmoid_grad64(c, gw):
+    """(gradient, bound) of the sigmoid form where sigmoids are close to 1: the
+    slope 1 - sigmoid(l) is taken as sigmoid(-l) on both sides, and every bound
+    carries it.  As above, with rel(slope) <= (2 max|l| + 10) u on top."""
+    T, E = c.l.shape
+    counts, tokens, _, _ = loss64(c.l, c.ids, c.k, c.off, "sigmoid")
+    spread = 2 * np.abs(np.where(np.isfinite(c.l), c.l, 0)).max()
+    relp = E / 32 + 16 + spread
+    grad, err = np.zeros((T, E)), np.zeros((T, E))
+    for s in range(c.S):
+        t = np.arange(c.off[s], c.off[s + 1])
+        t = t[((c.ids[t, :c.k] >= 0) & (c.ids[t, :c.k] < E)).any(axis=1)]
+        if not len(t):
+            continue
+        l = c.l[t].astype(np.float64)
+        p = scores64(c.l[t], "sigmoid")[1]
+        with np.errstate(over="ignore"):
+            slope = 1.0 / (1.0 + np.exp(l))
+        n = counts[s].astype(np.float64)[None]
+        coef = float(c.gl[s]) * E / (c.k * float(tokens[s]) ** 2)
+        dot = (p * n).sum(axis=1, keepdims=True)
+        grad[t] = coef * p * (n - dot) * slope
+        err[t] = abs(coef) * p * (n + dot) * slope * (2 * relp + E / 32 + 30 + spread)
+        if gw:
+            w, _, ok = weights64(c.l[t], c.ids[t], c.k, "sigmoid")
+            at = np.clip(c.ids[t, :c.k], 0, E - 1)
+            own = np.take_along_axis(slope, at, axis=1)
+            g = np.where(ok, c.gw[t].astype(np.float64), 0)
+            d = w * (g - (g * w).sum(axis=1, keepdims=True)) * own
+            e = w * (np.abs(g) + (np.abs(g) * w).sum(axis=1, keepdims=True)) * own * (66 + 2 * spread)
+            for j in range(c.k):
+                np.add.at(grad, (t, at[:, j]), np.where(ok[:, j], d[:, j], 0))
+                np.add.at(err, (t, at[:, j]), np.where(ok[:, j], e[:, j], 0))
+    return grad, err
+
+
+@pytest.mark.parametrize("lo,hi", [(8, 14), (14, 30), (-30, 30), (40, 80), (-5, 16)])
+@pytest.mark.parametrize("T,E,k", [(40, 64, 4), (33, 130, 6), (300, 384, 6), (21, 1023, 7)])
+def test_saturated_sigmoids_keep_their_slope(T, E, k, lo, hi):
+    """Gradients of experts whose sigmoid is 1 in fp32: their slope e^-l is
+    far from 0, and the gradient has it to fp32 accuracy."""
+    c = Case(T, E, k, S=2, scoring="sigmoid", seed=E + hi, pad=0.1)
+    c.l = np.random.default_rng(hi).uniform(lo, hi, (T, E)).astype(np.float32)
+    for gw in (True, False):
+        got = c.backward(gw)
+        want, err = sigmoid_grad64(c, gw)
+        assert (want != 0).any()
+        bad = np.abs(got - want) > err * U + 1e-37
+        assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], (err * U)[bad][:4])
