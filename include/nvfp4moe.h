@@ -439,8 +439,9 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
  *   probs  [S, E] fp32   P[e] = sum over those tokens of p[t, e]
  *   loss   [S] fp32      E / (k n^2) * sum_e counts[e] * P[e]   (0 when n = 0;
  *                        1 at perfect balance; callers weight and add them)
- * A logit of -inf has p = 0 (a row of -inf alone: p = 0 everywhere); logits
- * must not be NaN or +inf.  Sums are fp32 within a chunk of tokens and 64 bits
+ * A logit of -inf has p = 0 (a row of -inf alone: p = 0 everywhere), and so
+ * has, for sigmoids, one below -1e30; other rows have their shares however low
+ * the logits are.  Logits must not be NaN or +inf.  Sums are fp32 within a chunk of tokens and 64 bits
  * over the chunks, in a fixed order.  The workspace (caller-owned,
  * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
  * scratch: calls sharing one must not overlap on the device.

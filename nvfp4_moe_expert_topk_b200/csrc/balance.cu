@@ -124,6 +124,62 @@ __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &complemen
     complement = x < 0.0f ? large : small;
 }
 
+// 1 / x, 0 for 0.
+__device__ __forceinline__ float inverse(float x)
+{
+    return x == 0.0f ? 0.0f : __frcp_rn(x);
+}
+
+// Rows of low sigmoids.  Where sigmoids that are to be divided by their sum are
+// all below kTiny (a sum below it says so), they are e^l to fp32 accuracy and
+// their slopes 1: e^(l - max l) then takes their place, which fp32 holds however
+// low the logits are.  Below kMasked (a mask of the type's lowest value) a logit
+// counts as -inf.  Such rows are rare: the main loops leave them out, and a warp
+// that met one goes over its tokens again behind its loop (handled in the loop
+// they cost all other rows 3 to 8 %).  Both times the sum is taken by the same
+// steps, so that they agree on which rows these are.
+constexpr float kTiny = 1.0f / (1 << 30), kMasked = -1e30f;
+
+// 1 / sum of a row's scores, 0 for a row that is left out.
+template <bool SIG>
+__device__ __forceinline__ float inverse_sum(float sum)
+{
+    return SIG ? (sum < kTiny ? 0.0f : __frcp_rn(sum)) : inverse(sum);
+}
+
+__device__ __forceinline__ float low_score(float l, float m)
+{
+    return l < kMasked ? 0.0f : exp_fast(l - m);
+}
+
+// out[e] += the row's share of e (counts null), or its gradient of the loss for
+// counts and their coefficient; the whole warp.
+__device__ __forceinline__ void add_low_row(const float *row, int E, int lane, const int32_t *counts, float coef,
+                                            float *out)
+{
+    float m = -INFINITY, sum = 0.0f, dot = 0.0f;
+#pragma unroll 1
+    for (int c = lane; c < E; c += 32)
+        m = row[c] < kMasked ? m : fmaxf(m, row[c]);
+    m = warp_max(m);
+    if (m == -INFINITY)                            // nothing but masks
+        return;
+#pragma unroll 1
+    for (int c = lane; c < E; c += 32) {
+        const float v = low_score(row[c], m);
+        sum += v;
+        if (counts != nullptr)
+            dot = fmaf(v, coef * static_cast<float>(counts[c]), dot);
+    }
+    const float inv = inverse(warp_sum(sum));
+    dot = warp_sum(dot) * inv;
+#pragma unroll 1
+    for (int c = lane; c < E; c += 32) {
+        const float p = low_score(row[c], m) * inv;
+        out[c] += counts == nullptr ? p : p * (coef * static_cast<float>(counts[c]) - dot);
+    }
+}
+
 // Start of sequence s (s = S: end of the last), clamped into [0, T].
 __device__ __forceinline__ int seq_start(const BalanceArgs &a, int s)
 {
@@ -218,13 +274,23 @@ struct Row {
         }
         return sum;
     }
+    // sigmoids, each passed to f, and the lane's part of their sum; in place stays the smaller one of the score and
+    // its complement (their product is the slope)
+    template <typename F>
+    __device__ __forceinline__ float sigmoids(F f)
+    {
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4 * P; ++q) {
+            float s, complement;
+            sigmoid_pair(v[q], s, complement);
+            sum += s;
+            f(q, s);
+            v[q] = fminf(s, complement);
+        }
+        return sum;
+    }
 };
-
-// 1 / x, 0 for 0.
-__device__ __forceinline__ float inverse(float x)
-{
-    return x == 0.0f ? 0.0f : __frcp_rn(x);
-}
 
 } // namespace
 
@@ -292,6 +358,7 @@ __global__ void __launch_bounds__(32 * chunk_warps(P, WHOLE), WHOLE ? 1 : chunk_
     for (int q = 0; q < 4 * P; ++q)
         acc[q] = 0.0f;
     int tokens = 0;
+    bool low = false;
     for (int tb = t0 + warp; tb < t1; tb += D * W) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
@@ -305,7 +372,8 @@ __global__ void __launch_bounds__(32 * chunk_warps(P, WHOLE), WHOLE ? 1 : chunk_
                 ++tokens;
                 if (on)
                     atomicAdd(hist + id, 1);
-                const float inv = inverse(warp_sum(r.template scores<SIG>()));
+                const float sum = warp_sum(r.template scores<SIG>()), inv = inverse_sum<SIG>(sum);
+                low |= SIG && sum < kTiny;
 #pragma unroll
                 for (int q = 0; q < 4 * P; ++q)
                     acc[q] = fmaf(r.v[q], inv, acc[q]);
@@ -320,6 +388,20 @@ __global__ void __launch_bounds__(32 * chunk_warps(P, WHOLE), WHOLE ? 1 : chunk_
         const int c = Row<P, V4>::col(lane, q);
         if (c < E)
             sm[warp * E + c] = acc[q];
+    }
+    if (SIG && low) {
+        __syncwarp();
+#pragma unroll 1
+        for (int t = t0 + warp; t < t1; t += W) {
+            const int id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
+            const float *row = a.logits + static_cast<int64_t>(t) * E;
+            if (!__any_sync(kAll, id >= 0 && id < E))
+                continue;
+            Row<P, V4> r;
+            r.load(row, E, lane);
+            if (warp_sum(r.template scores<true>()) < kTiny)
+                add_low_row(row, E, lane, nullptr, 0.0f, sm + warp * E);
+        }
     }
     __syncthreads();
     pdl_trigger();                                 // (the next kernel's blocks would only be in the way before)
@@ -502,6 +584,19 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
     constexpr bool kHold = P <= 3;
     int s = -1, s_end = 0;
     float cnt[kHold ? 4 * P : 1] = {}, coef = 0.0f;
+    // the last sequence that starts at or before t (and is not empty there), its coefficient; false: t is outside
+    // every sequence, or the sequence has no tokens
+    auto enter = [&](int t) {
+        s = last_sequence(a.S, lane, [&](int i) { return seq_start(a, i) <= t; });
+        s_end = seq_start(a, s + 1);
+        const int n = __ldg(a.tokens + s);
+        const bool in = t >= seq_start(a, s) && t < s_end && n > 0;
+        coef = in ? static_cast<float>(static_cast<double>(__ldg(a.grad_loss + s)) * E /
+                                       (static_cast<double>(a.k) * n * n))
+                  : 0.0f;
+        return in;
+    };
+    bool low = false;                              // a row's scores or its selected ones are left for later
     auto count = [&](int q) -> float {
         if (kHold)
             return cnt[kHold ? q : 0];
@@ -532,14 +627,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
         if (t >= t_end)
             break;
         if (s < 0 || t >= s_end) {
-            // the last sequence that starts at or before t (and is not empty there)
-            s = last_sequence(a.S, lane, [&](int i) { return seq_start(a, i) <= t; });
-            s_end = seq_start(a, s + 1);
-            const int n = __ldg(a.tokens + s);
-            const bool in = t >= seq_start(a, s) && t < s_end && n > 0;
-            coef = in ? static_cast<float>(static_cast<double>(__ldg(a.grad_loss + s)) * E /
-                                           (static_cast<double>(a.k) * n * n))
-                      : 0.0f;
+            const bool in = enter(t);
             if (kHold)
 #pragma unroll
                 for (int q = 0; q < 4 * P; ++q) {
@@ -563,16 +651,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
             float sums[4];
             sums[1] = 0.0f;
             if (SIG) {
-                // in place: the smaller one of the score and its complement (their product is the slope)
-                sums[0] = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 4 * P; ++q) {
-                    float sc, comp;
-                    sigmoid_pair(r.v[q], sc, comp);
-                    sums[0] += sc;
-                    sums[1] = fmaf(sc, count(q), sums[1]);
-                    r.v[q] = fminf(sc, comp);
-                }
+                sums[0] = r.sigmoids([&](int q, float sc) { sums[1] = fmaf(sc, count(q), sums[1]); });
             } else {
                 sums[0] = r.template scores<false>();
 #pragma unroll
@@ -593,8 +672,9 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
             sums[3] = on ? g * v : 0.0f;
             warp_sum4(sums);
             // p (c - sum p c) coef with p = score * inv and the counts scaled by coef: score (inv c' - inv dot)
-            const float inv = inverse(sums[0]);
+            const float inv = inverse_sum<SIG>(sums[0]);
             const float dot = -sums[1] * inv * inv;
+            low |= SIG && (sums[0] < kTiny || (a.grad_weights != nullptr && sums[2] < kTiny));
 #pragma unroll
             for (int q = 0; q < 4 * P; ++q) {
                 const float sc = r.v[q];
@@ -604,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
             }
             if (a.grad_weights != nullptr) {
                 // w (g - sum g w) with w = v / sum v
-                const float q = inverse(sums[2]);
+                const float q = inverse_sum<SIG>(sums[2]);
                 const float d = v * q * (g - sums[3] * q) * slope;
                 // into the row by way of shared memory; slots of one expert add up in slot order
                 // (found by the slots' numbers: comparing them by shuffles took 40 instructions more, 48.5 us
@@ -661,6 +741,36 @@ __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward
         fetch(u, D, t + D);
         at += E;
         id_at += a.ld_ids;
+    }
+    if (SIG && low) {
+#pragma unroll 1
+        for (int t = static_cast<int>(tw); t < t_end; ++t) {
+            const int id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.ld_ids + lane) : -1;
+            const bool on = id >= 0 && id < E;
+            if (!__any_sync(kAll, on) || !enter(t))
+                continue;
+            const float *row = a.logits + static_cast<int64_t>(t) * E;
+            float *out = a.grad_logits + static_cast<int64_t>(t) * E;
+            const float l = on ? __ldg(row + id) : -INFINITY;
+            Row<P, V4> r;
+            r.load(row, E, lane);
+            float sums[4] = {r.sigmoids([](int, float) {}), 0.0f, 0.0f, 0.0f}, slope;
+            sigmoid_pair(l, sums[2], slope);
+            warp_sum4(sums);
+            __syncwarp();                          // (the row as it was stored above)
+            if (sums[0] < kTiny)
+                add_low_row(row, E, lane, a.counts + static_cast<int64_t>(s) * E, coef, out);
+            const float m = warp_max(l < kMasked ? -INFINITY : l);
+            if (a.grad_weights == nullptr || !(sums[2] < kTiny) || m == -INFINITY)
+                continue;
+            const float g = on ? __ldg(a.grad_weights + static_cast<int64_t>(t) * a.k + lane) : 0.0f;
+            const float v = low_score(l, m), q = inverse(warp_sum(v)), dot = warp_sum(g * v) * q;
+            for (int j = 0; j < a.k; ++j) {        // in slot order
+                __syncwarp();
+                if (lane == j && on)
+                    out[id] += v * q * (g - dot);
+            }
+        }
     }
 }
 

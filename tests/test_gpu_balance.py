@@ -546,3 +546,99 @@ def test_saturated_sigmoids_keep_their_slope(T, E, k, lo, hi):
         assert (want != 0).any()
         bad = np.abs(got - want) > err * U + 1e-37
         assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], (err * U)[bad][:4])
+
+
+def check_low(c):
+    """Case.check for sigmoids that fp32 does not hold.  A score below 2^-126 is
+    0 (of a row that is taken relative to its largest logit: below 2^-126 of that
+    one's), so a share p is off by up to 2^-126 / sum of the scores beside its
+    rounding; a gradient entry by that times |coef| (max count + sum p count), a
+    weight's part by that, over the selected, times |g| + sum |g| w."""
+    counts, tokens, P, loss = (t.cpu().numpy() for t in c.forward())
+    wc, wt, wP, wl = loss64(c.l, c.ids, c.k, c.off, "sigmoid")
+    np.testing.assert_array_equal(counts, wc)
+    np.testing.assert_array_equal(tokens, wt)
+
+    def flush(total):
+        return 2.0 ** -126 / np.where(total < 2.0 ** -31, 1.0, total)
+    sc, p = scores64(c.l, "sigmoid")
+    lost = flush(sc.sum(axis=1, keepdims=True))
+    rel = (c.E / 32 + 16 + 2 * np.abs(c.l).max() + chunk_bound(c.T) / 8 + 14) * U
+    np.testing.assert_allclose(P, wP, rtol=rel, atol=c.T * lost.max())
+    np.testing.assert_allclose(loss, wl, rtol=rel, atol=1e-37)
+    seq = np.clip(np.searchsorted(c.off, np.arange(c.T), side="right") - 1, 0, c.S - 1)
+    n = wc[seq].astype(np.float64)
+    coef = np.abs(c.gl[seq]) * c.E / (c.k * np.maximum(wt[seq], 1).astype(np.float64) ** 2)
+    slack = coef[:, None] * (n.max(axis=1, keepdims=True) + (p * n).sum(axis=1, keepdims=True)) * lost
+    w, _, ok = weights64(c.l, c.ids, c.k, "sigmoid")
+    sel = np.where(ok, np.take_along_axis(sc, np.clip(c.ids[:, :c.k], 0, c.E - 1), axis=1), 0).sum(axis=1, keepdims=True)
+    g = np.abs(np.where(ok, c.gw, 0)).astype(np.float64)
+    part = c.k * (g.max(axis=1, keepdims=True) + (g * w).sum(axis=1, keepdims=True)) * flush(sel)
+    for gw in (True, False):
+        got = c.backward(gw)
+        want, err = grad64(c.l, c.ids, c.k, c.off, "sigmoid", c.gl, c.gw if gw else None)
+        bad = np.abs(got - want) > err * U + slack + (part if gw else 0) + 1e-37
+        assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], (err * U)[bad][:4])
+    return counts, tokens, P, loss
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 72, 4), (33, 130, 6), (700, 384, 6), (300, 48, 6), (21, 1023, 7)])
+def test_sigmoids_far_below_one(T, E, k):
+    """Rows of which every sigmoid is below what fp32 holds, or close to it:
+    their shares are well defined, those of e^l.  Logits around -88, -150 and
+    around the border where rows are taken relative to their largest logit."""
+    for lo, hi in ((-95, -80), (-160, -140), (-27, -18), (-120, 3)):
+        c = Case(T, E, k, S=2, scoring="sigmoid", seed=E - hi, pad=0.1)
+        c.l = np.random.default_rng(-lo).uniform(lo, hi, (T, E)).astype(np.float32)
+        c.l[::5] += 100.0                                # ordinary rows between them
+        counts, tokens, P, loss = check_low(c)
+        assert (P[tokens > 0].sum(axis=1) > 0.999 * tokens[tokens > 0]).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(50, 64, 4), (700, 130, 6)])
+def test_sigmoids_of_very_low_logits(T, E, k):
+    """Around -2000 a sigmoid is e^l to any accuracy, so the sigmoid form is the
+    softmax form; masked places among them stay without a share."""
+    rng = np.random.default_rng(E)
+    c = Case(T, E, k, S=2, scoring="sigmoid", seed=E)
+    c.l = rng.normal(-2000, 2, (T, E)).astype(np.float32)
+    m = rng.random((T, E)) < 0.3
+    m[np.arange(T)[:, None], c.ids] = False
+    for mask in (-np.inf, np.finfo(np.float32).min):
+        c.l[m] = mask
+        low = np.where(m, -np.inf, c.l).astype(np.float32)
+        counts, tokens, P, loss = (t.cpu().numpy() for t in c.forward())
+        wc, wt, wP, wl = loss64(low, c.ids, k, c.off, "softmax")
+        np.testing.assert_array_equal(counts, wc)
+        rel = (E / 32 + 16 + 60 + chunk_bound(T) / 8 + 14) * U       # logits of a row are within 30
+        np.testing.assert_allclose(P, wP, rtol=rel, atol=1e-37)
+        np.testing.assert_allclose(loss, wl, rtol=rel, atol=1e-37)
+        for gw in (True, False):
+            got = c.backward(gw)
+            want, err = grad64(low, c.ids, k, c.off, "softmax", c.gl, c.gw if gw else None)
+            assert (want != 0).any() and (np.abs(got - want) <= err * U + 1e-37).all()
+
+
+def test_slots_far_below_the_rest_of_their_row():
+    """The selected experts' sigmoids vanish beside the row's others: the
+    weights among them are still those of their logits."""
+    c = Case(80, 40, 4, S=2, scoring="sigmoid", seed=3)
+    rng = np.random.default_rng(3)
+    at = np.arange(80)[:, None]
+    c.l[at, c.ids] = rng.uniform(-130, -90, (80, 4)).astype(np.float32)
+    c.ids[::7, 1] = -1
+    c.ids[::9, 2] = c.ids[::9, 0]
+    check_low(c)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (130, 4), (384, 6), (1000, 8)])
+def test_sums_of_sigmoids_at_the_border(E, k):
+    """Rows whose sigmoids add up to 2^-30 within a few roundings, where one
+    form of a row gives way to another: each row is counted once."""
+    T = 600
+    c = Case(T, E, k, S=2, scoring="sigmoid", seed=E)
+    l = np.random.default_rng(E).normal(0, 1, (T, E))
+    sums = np.exp(l).sum(axis=1, keepdims=True)
+    c.l = (l - np.log(sums) - 30 * np.log(2.0) + np.linspace(-4e-6, 4e-6, T)[:, None]).astype(np.float32)
+    counts, tokens, P, loss = check_low(c)
+    assert np.abs(P.sum(axis=1) - tokens).max() < 1e-3 * T
