@@ -444,7 +444,8 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
  * the logits are.  Logits must not be NaN or +inf.  Sums are fp32 within a chunk of tokens and 64 bits
  * over the chunks, in a fixed order.  The workspace (caller-owned,
  * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
- * scratch: calls sharing one must not overlap on the device.
+ * scratch: calls sharing one must not overlap on the device.  The size does not
+ * shrink as T, S or E grow, so a workspace of the largest batch serves all.
  * 1 <= k <= min(E, 32), E <= 1024, 1 <= S <= 65535, T >= 0 (T = 0: logits and
  * topk_ids may be NULL; zeros are written).  One launch for short
  * batches, two otherwise. */

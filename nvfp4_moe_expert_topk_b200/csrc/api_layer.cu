@@ -19,7 +19,8 @@ int status_of(cudaError_t e)
 }
 
 // Workspace of nvfp4_moe_balance: per chunk slot E probability sums and E
-// counts (padded to 4) and the token count.
+// counts (padded to 4) and the token count; as many slots as any batch that is
+// no larger takes.
 struct BalanceLayout {
     int64_t part_c, part_n, total;
 };
@@ -27,7 +28,7 @@ struct BalanceLayout {
 BalanceLayout balance_layout(int64_t T, int64_t S, int64_t E)
 {
     BalanceLayout L;
-    const int64_t slots = balance_slots(T, S, static_cast<int>(E)), row = (E + 3) / 4 * 16;
+    const int64_t slots = balance_slots_most(T, S), row = (E + 3) / 4 * 16;
     L.part_c = slots * row;
     L.part_n = 2 * L.part_c;
     L.total = L.part_n + 4 * slots;

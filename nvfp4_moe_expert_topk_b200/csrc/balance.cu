@@ -793,6 +793,17 @@ int64_t balance_slots(int64_t T, int64_t S, int E)
     return T / balance_chunk(T, S, E) + S;
 }
 
+// At least as many as any batch of up to T tokens in up to S sequences takes,
+// for any E (12 tokens per chunk at least, at most 2 blocks per SM): what the
+// workspace holds.  It does not shrink as T or S grow, which the slots of one
+// batch do where its chunks get longer.
+int64_t balance_slots_most(int64_t T, int64_t S)
+{
+    constexpr int64_t fit = 148 * 2;
+    const int64_t blocks = S < fit / 2 ? fit - S : fit / 2;
+    return (T / 12 < blocks ? T / 12 : blocks) + S;
+}
+
 // 16-byte loads and stores need every row to start on a 16-byte boundary.
 static bool aligned_rows(const BalanceArgs &a)
 {

@@ -244,6 +244,7 @@ struct BalanceArgs {
 };
 int balance_chunk(int64_t T, int64_t S, int E);
 int64_t balance_slots(int64_t T, int64_t S, int E);
+int64_t balance_slots_most(int64_t T, int64_t S);
 cudaError_t launch_balance(const BalanceArgs &args, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs &args, cudaStream_t s);
 

@@ -642,3 +642,17 @@ def test_sums_of_sigmoids_at_the_border(E, k):
     c.l = (l - np.log(sums) - 30 * np.log(2.0) + np.linspace(-4e-6, 4e-6, T)[:, None]).astype(np.float32)
     counts, tokens, P, loss = check_low(c)
     assert np.abs(P.sum(axis=1) - tokens).max() < 1e-3 * T
+
+
+def test_one_workspace_for_all_batch_lengths():
+    """Sized for the longest batch, with no shorter one refused, and the same
+    results as on a workspace of their own."""
+    ws = torch.empty(nvfp4_moe_balance_workspace_size(3000, 4, 384), dtype=torch.uint8, device=DEV)
+    for T, S in ((2048, 1), (2000, 0), (2049, 1), (3000, 4), (17, 2), (1500, 3)):
+        c = Case(T, 384, 6, S=S, seed=T)
+        l, ids, o = c.dev()
+        out = [torch.empty(c.S, 384, dtype=torch.int32, device=DEV), torch.empty(c.S, dtype=torch.int32, device=DEV),
+               torch.empty(c.S, 384, device=DEV), torch.empty(c.S, device=DEV)]
+        nvfp4_moe_balance(l, ids, 6, *out, ws, seq_offsets=o)
+        for a, b in zip(out, c.forward()):
+            assert torch.equal(a, b)

@@ -183,3 +183,28 @@ def test_binding_argument_kinds(L):
         with pytest.raises(ValueError):
             pkg.nvfp4_add_rmsnorm(x, x, 1e-6, y=x, residual=x, residual_out=x, codes=x, scales=x, gs=x)
     assert sys.getrefcount(x) == before
+
+
+@pytest.mark.parametrize("S", [1, 2, 4, 33, 147, 148, 149, 1000])
+@pytest.mark.parametrize("E", [1, 48, 384, 512, 513, 1024])
+def test_balance_workspace_of_a_long_batch_serves_shorter_ones(L, E, S):
+    """A caller sizes its workspace once, for its largest batch: the size does
+    not shrink as T, S or E grow (every T over the borders between chunk lengths)."""
+    n = L.nvfp4_moe_balance_workspace_size
+    last = 0
+    around = [128 * w * S + d for w in (12, 16) for d in (-1, 0, 1)]
+    for T in sorted(set(range(6000)) | set(range(6000, 300000, 997)) | set(around)):
+        assert n(T, S, E) >= last, T
+        last = n(T, S, E)
+    for T in (1, 700, 2000, 128 * 12 * S, 128 * 16 * S, 128 * 16 * S + 1, 100000):
+        assert n(T, S, E) <= n(T, S + 1, E) and n(T, S, E) <= n(T + 1, S, E)
+        if E < 1024:
+            assert n(T, S, E) <= n(T, S, E + 1)
+
+
+def test_balance_takes_a_workspace_of_a_longer_batch(L):
+    if not no_device():
+        pytest.skip("the pointers of this test are not real")
+    size = max(L.nvfp4_moe_balance_workspace_size(3000, 1, 384), L.nvfp4_moe_balance_workspace_size(2049, 1, 384))
+    for T in (1, 100, 1999, 2000, 2047, 2048, 2049, 3000):
+        assert balance(L, T=T, E=384, off=None, S=1, nbytes=size) in OK_BUT_NO_DEVICE, T
