@@ -416,12 +416,22 @@ int nvfp4_add_rmsnorm(const nvfp4_norm_args *args, void *stream);
  * out [M, ldo] bf16, ldo >= N; only the [M, N] window is written.
  * Constraints: 0 <= M <= 16 (0 launches nothing; x and out may then be NULL),
  * N >= 1, K % 64 == 0, K <= 1 << 20, 1 <= nseg <= 4; x, b_codes, b_scales
- * 16-byte aligned.  Inputs must be finite (a row of x that is not spoils that
- * row of out only). */
+ * 16-byte aligned; out must not overlap the inputs.  Inputs must be finite (a
+ * row of x that is not spoils that row of out only).  Waits on the weights'
+ * copies are bounded (2 s); outputs that lack weights because one gave up are
+ * NaN. */
 int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx,
                const uint8_t *b_codes, const uint8_t *b_scales, const float *b_gs,
                const int64_t *seg_end, int nseg, int64_t N, int64_t K,
                uint16_t *out, int64_t ldo, void *stream);
+
+/* Test hook for failure detection: nvfp4_gemv, except that one wait on the
+ * weights' copies (of the rows n = 0 .. 7, 32 .. 39, 64 .. 71 and 96 .. 103 at
+ * least) runs out.  Takes some seconds; no fault and no trap. */
+int nvfp4_debug_gemv_timeout(const uint16_t *x, int64_t M, int64_t ldx,
+                             const uint8_t *b_codes, const uint8_t *b_scales, const float *b_gs,
+                             const int64_t *seg_end, int nseg, int64_t N, int64_t K,
+                             uint16_t *out, int64_t ldo, void *stream);
 
 /* Load statistics and balance loss of the router, per sequence.  logits
  * [T, E] fp32 and topk_ids [T, ld_ids] as nvfp4_moe_topk reads and writes them

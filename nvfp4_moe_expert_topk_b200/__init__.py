@@ -24,6 +24,7 @@ __all__ = [
     "nvfp4_moe_get_error", "nvfp4_moe_topk", "nvfp4_moe_topk_shared", "NVFP4_SCORING_SOFTMAX",
     "NVFP4_SCORING_SIGMOID", "nvfp4_fp4_mma_ceiling", "nvfp4_tma_stream_ceiling", "nvfp4_moe_plan", "nvfp4_amax", "nvfp4_debug_bounded_wait",
     "MoeArgs", "NVFP4_QUANT_NONE", "NVFP4_QUANT_NVFP4", "NVFP4_QUANT_E4M3", "nvfp4_add_rmsnorm", "nvfp4_gemv",
+    "nvfp4_debug_gemv_timeout",
     "nvfp4_moe_balance_workspace_size", "nvfp4_moe_balance", "nvfp4_moe_balance_backward", "NormArgs",
 ]
 
@@ -107,6 +108,7 @@ def lib():
                                      ctypes.POINTER(ctypes.c_int32)]
         L.nvfp4_add_rmsnorm.argtypes = [ctypes.POINTER(NormArgs), P]
         L.nvfp4_gemv.argtypes = [P, i64, i64, P, P, P, ctypes.POINTER(i64), i32, i64, i64, P, i64, P]
+        L.nvfp4_debug_gemv_timeout.argtypes = L.nvfp4_gemv.argtypes
         L.nvfp4_moe_balance_workspace_size.argtypes = [i64, i64, i32]
         L.nvfp4_moe_balance_workspace_size.restype = ctypes.c_size_t
         L.nvfp4_moe_balance.argtypes = [P, P, i64, i64, i32, i32, P, i64, i32, P, P, P, P, P, ctypes.c_size_t, P]
@@ -404,6 +406,17 @@ def nvfp4_gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
     st = (_native or _binding()).gemv(x, b_codes, b_scales, b_gs, seg_end, out, stream)
     if st != 0:
         raise Nvfp4Error(st, "nvfp4_gemv")
+
+
+def nvfp4_debug_gemv_timeout(x, b_codes, b_scales, b_gs, seg_end, out, stream=None):
+    """nvfp4_gemv (contiguous rows) with one wait on the weights' copies that
+    runs out: the outputs of at least the rows 0 .. 7 of B become NaN."""
+    (M, K), N = x.shape, b_codes.shape[0]
+    seg = (ctypes.c_int64 * len(seg_end))(*seg_end)
+    _check(lib().nvfp4_debug_gemv_timeout(_dev(x, "x", torch.bfloat16), M, K, _dev(b_codes, "b_codes", torch.uint8),
+                                          _dev(b_scales, "b_scales", torch.uint8), _dev(b_gs, "b_gs", torch.float32), seg,
+                                          len(seg_end), N, K, _dev(out, "out", torch.bfloat16), N, _stream(stream)),
+           "nvfp4_debug_gemv_timeout")
 
 
 def nvfp4_moe_balance_workspace_size(T, S, E):

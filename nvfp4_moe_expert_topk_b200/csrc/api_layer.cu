@@ -46,6 +46,54 @@ int check_balance(int64_t T, int64_t S, int E, int k, int64_t ld_ids, int scorin
     return NVFP4_OK;
 }
 
+int gemv(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_scales, const float *b_gs,
+         const int64_t *seg_end, int nseg, int64_t N, int64_t K, uint16_t *out, int64_t ldo, int withhold, void *stream)
+{
+    if (M < 0 || N < 1 || K < 1 || nseg < 1 || seg_end == nullptr)
+        return NVFP4_ERR_INVALID_ARG;
+    if (b_codes == nullptr || b_scales == nullptr || b_gs == nullptr)
+        return NVFP4_ERR_INVALID_ARG;
+    if (M > 0 && (x == nullptr || out == nullptr || ldx < K || ldo < N))
+        return NVFP4_ERR_INVALID_ARG;
+    if (M > kGemvMaxRows || K % 64 != 0 || K > (1LL << 20) || N > (1LL << 30) || nseg > 4 ||
+        (N + 127) / 128 * (K / 64) >= (1LL << 31))
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    int64_t prev = 0;
+    for (int i = 0; i < nseg; ++i) {
+        if (seg_end[i] <= prev)
+            return NVFP4_ERR_INVALID_ARG;
+        prev = seg_end[i];
+    }
+    if (prev != N)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(b_codes, 16) || !aligned(b_scales, 16) || !aligned(b_gs, 4))
+        return NVFP4_ERR_MISALIGNED;
+    if (M > 0 && (!aligned(x, 16) || !aligned(out, 2) || ldx % 8 != 0))
+        return NVFP4_ERR_MISALIGNED;
+    int sms = 0;
+    const int st = device_status(&sms);
+    if (st != NVFP4_OK)
+        return st;
+    if (M == 0)
+        return NVFP4_OK;
+    GemvArgs g{};
+    g.x = reinterpret_cast<const __nv_bfloat16 *>(x);
+    g.M = M;
+    g.ldx = ldx;
+    g.codes = b_codes;
+    g.scales = b_scales;
+    g.gs = b_gs;
+    g.nseg = nseg;
+    for (int i = 0; i < nseg; ++i)
+        g.seg_end[i] = seg_end[i];
+    g.N = N;
+    g.K = K;
+    g.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    g.ldo = ldo;
+    g.withhold = withhold;
+    return status_of(launch_gemv(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
 } // namespace
 
 extern "C" {
@@ -114,48 +162,14 @@ int nvfp4_gemv(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *b_codes
                const float *b_gs, const int64_t *seg_end, int nseg, int64_t N, int64_t K, uint16_t *out, int64_t ldo,
                void *stream)
 {
-    if (M < 0 || N < 1 || K < 1 || nseg < 1 || seg_end == nullptr)
-        return NVFP4_ERR_INVALID_ARG;
-    if (b_codes == nullptr || b_scales == nullptr || b_gs == nullptr)
-        return NVFP4_ERR_INVALID_ARG;
-    if (M > 0 && (x == nullptr || out == nullptr || ldx < K || ldo < N))
-        return NVFP4_ERR_INVALID_ARG;
-    if (M > kGemvMaxRows || K % 64 != 0 || K > (1LL << 20) || N > (1LL << 30) || nseg > 4 ||
-        (N + 127) / 128 * (K / 64) >= (1LL << 31))
-        return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    int64_t prev = 0;
-    for (int i = 0; i < nseg; ++i) {
-        if (seg_end[i] <= prev)
-            return NVFP4_ERR_INVALID_ARG;
-        prev = seg_end[i];
-    }
-    if (prev != N)
-        return NVFP4_ERR_INVALID_ARG;
-    if (!aligned(b_codes, 16) || !aligned(b_scales, 16) || !aligned(b_gs, 4))
-        return NVFP4_ERR_MISALIGNED;
-    if (M > 0 && (!aligned(x, 16) || !aligned(out, 2) || ldx % 8 != 0))
-        return NVFP4_ERR_MISALIGNED;
-    int sms = 0;
-    const int st = device_status(&sms);
-    if (st != NVFP4_OK)
-        return st;
-    if (M == 0)
-        return NVFP4_OK;
-    GemvArgs g{};
-    g.x = reinterpret_cast<const __nv_bfloat16 *>(x);
-    g.M = M;
-    g.ldx = ldx;
-    g.codes = b_codes;
-    g.scales = b_scales;
-    g.gs = b_gs;
-    g.nseg = nseg;
-    for (int i = 0; i < nseg; ++i)
-        g.seg_end[i] = seg_end[i];
-    g.N = N;
-    g.K = K;
-    g.out = reinterpret_cast<__nv_bfloat16 *>(out);
-    g.ldo = ldo;
-    return status_of(launch_gemv(g, sms, static_cast<cudaStream_t>(stream)));
+    return gemv(x, M, ldx, b_codes, b_scales, b_gs, seg_end, nseg, N, K, out, ldo, 0, stream);
+}
+
+int nvfp4_debug_gemv_timeout(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *b_codes, const uint8_t *b_scales,
+                             const float *b_gs, const int64_t *seg_end, int nseg, int64_t N, int64_t K, uint16_t *out,
+                             int64_t ldo, void *stream)
+{
+    return gemv(x, M, ldx, b_codes, b_scales, b_gs, seg_end, nseg, N, K, out, ldo, 1, stream);
 }
 
 size_t nvfp4_moe_balance_workspace_size(int64_t T, int64_t S, int E)

@@ -40,7 +40,7 @@
 // the order its lanes read it, and walks over row tiles.  k is split over the
 // blocks of a cluster and over the `slices` warps of a tile; partial sums meet
 // in shared memory in a fixed order.  Every wait on a copy is bounded: a warp
-// that gives up stops loading and ends with sums of what it has.
+// that gives up stops loading, and the sums it has a share in become NaN.
 //
 // Measured (one B200, calls back to back): 3 x 200 x 256 (M x N x K) 3.3 us, 1 x
 // 2048 x 7168 6.9 us, 5 x 7168 x 8192 14.0 us (2.4 TB/s), 16 x 65536 x 1536 20.2
@@ -318,6 +318,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         for (int u = 0; u < kKeep; ++u)
             keep[m][u] = warp + u * warps < (b1 - b0) * 8 ? piece(m, b0, warp + u * warps) : make_uint4(0, 0, 0, 0);
     asm volatile("" ::: "memory");
+    if (a.withhold && blockIdx.x == 0 && threadIdx.x == 0)
+        mbar_expect_tx(&bar[0], 16);               // bytes that never come
     if (whole) {
         share(b0, b1 - b0);
         f_end = pl.rounds;
@@ -504,6 +506,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     acc[p][0][0][v] += acc[p][0][kChains - 1][v];
+        if (__builtin_expect(!ok, 0))              // not all of the weights came
+#pragma unroll
+            for (int v = 0; v < kVals; ++v)
+                acc[v / (4 * MT)][v / 4 % MT][0][v & 3] = __int_as_float(0x7FC00000);
         const int tile = tile_of(it);
         if (pl.slices == 1 && cluster == 1) {
             // nothing to add up: straight from the registers

@@ -222,6 +222,7 @@ struct GemvArgs {
     int64_t N, K;
     __nv_bfloat16 *out;
     int64_t ldo;
+    int withhold;             // 1: a wait of the first block's first warp runs out (test hook)
 };
 cudaError_t launch_gemv(const GemvArgs &args, int num_sms, cudaStream_t s);
 // Router load statistics, balance loss and gradient (balance.cu).
