@@ -378,7 +378,8 @@ int nvfp4_moe_topk_shared(const float *logits, int64_t T, int E, int k, int scor
  *   NVFP4_QUANT_E4M3: codes [T, H] E4M3 bytes and scales float
  *          [T, ceil(H/128)], from the fp32 y (not its bf16 rounding): per 128
  *          columns a = max|y|, scale = a / 448, r = a == 0 ? 0 : 448 / a,
- *          code = E4M3(y * r) (nearest even); value = code * scale
+ *          code = E4M3(y * r) (nearest even); value = code * scale (where
+ *          448 / a passes the fp32 range: the product as if it did not)
  * The results do not depend on T, on a row's place in the batch or on the
  * launch shape.  Strides are in elements; rows may be strided (ld >= H).
  * Aliases: residual_out may be residual or x, and y may be x or residual

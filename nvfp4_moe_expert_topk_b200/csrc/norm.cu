@@ -221,7 +221,14 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 3 : VPT == 2 ? 2 : 1) add_rmsn
             for (int o = 1; o < 8; o <<= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (on) {
-                const float r = m == 0.0f ? 0.0f : __fdiv_rn(448.0f, m);
+                float top = m;
+                if (m < 0x1p-100f) {               // 448 / m may not be an fp32 number: both sides times 2^100, exactly
+                    top *= 0x1p100f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        f[j] *= 0x1p100f;
+                }
+                const float r = m == 0.0f ? 0.0f : __fdiv_rn(448.0f, top);
                 uint32_t q[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

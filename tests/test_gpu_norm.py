@@ -281,3 +281,40 @@ def test_binding_refusals():
         args.update(change)
         with pytest.raises(ValueError, match=match):
             nvfp4_add_rmsnorm(**args)
+
+
+@pytest.mark.parametrize("H", [128, 208, 7168])
+@pytest.mark.parametrize("low", [2.0 ** -126, 2.0 ** -118, 1e-36, 2.0 ** -100, 2.0 ** -99])
+def test_e4m3_groups_of_tiny_values(H, low):
+    """Groups whose largest magnitude is so small that 448 / a is not an fp32
+    number, zeros among them (a dead channel group beside live ones): each
+    code is E4M3 of y * 448 / a, taken here in 64 bits.  The quotient and the
+    product each round by 2^-24, so a code is one of the two E4M3 neighbours
+    of a value within that of a border between them."""
+    T = 6
+    x = rows(T, H, 3)
+    w = torch.ones(H, dtype=torch.bfloat16)
+    dead = slice(0, 128) if H > 128 else slice(0, 0)     # (one group alone: the weight is small instead)
+    g = torch.Generator().manual_seed(1)
+    tiny = (torch.randn(H, generator=g) * low).to(torch.bfloat16)
+    tiny[::3] = 0.0
+    if H > 128:
+        x[:, dead] = tiny[dead]
+        x[1, dead] = 0.0
+    else:
+        w = tiny
+    codes = torch.empty(T, H, dtype=torch.float8_e4m3fn, device=DEV)
+    scales = torch.empty(T, (H + 127) // 128, device=DEV)
+    nvfp4_add_rmsnorm(x.to(DEV), w.to(DEV), EPS, quant=NVFP4_QUANT_E4M3, codes=codes, scales=scales)
+    _, y = reference(x, None, w)
+    got = codes.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    for i in range(0, H, 128):
+        v = y[:, i:i + 128].astype(np.float64)
+        a = np.abs(v).max(axis=1, keepdims=True)
+        assert np.array_equal(scales[:, i // 128].cpu().numpy(), (y[:, i:i + 128].__abs__().max(axis=1) / np.float32(448.0)))
+        want = v * np.where(a > 0, 448.0 / np.where(a > 0, a, 1), 0)
+        for sign in (-1, 1):                             # one of the codes of want (1 -+ 2^-22)
+            near = torch.from_numpy(want * (1 + sign * 2.0 ** -22)).clamp(-448, 448).to(torch.float8_e4m3fn).double().numpy()
+            side = near if sign < 0 else np.where(got[:, i:i + 128] == side, side, near)
+        assert np.array_equal(got[:, i:i + 128], side)
