@@ -61,8 +61,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    build_binding(force, verbose)
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compiles the CUDA sources (nvcc alone: neither torch nor its headers)."""
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -79,6 +79,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB + ".tmp"
     subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """The library, then the Python module.  Where the module cannot be built
+    (no torch, no host compiler) the library is there all the same, and the
+    entry points that need the module say that it is missing."""
+    build_library(force, verbose, ptxas_info)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        for path in (BINDING, BINDING + ".torch"):       # none of older sources
+            if os.path.exists(path):
+                os.remove(path)
+        print(f"{BINDING} was not built: {e}", file=sys.stderr)
     return LIB
 
 
