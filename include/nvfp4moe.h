@@ -110,7 +110,9 @@ int nvfp4_swizzle_scales(const uint8_t *in, int64_t batch, int64_t rows, int64_t
  * equal to N, each a multiple of 32; rows of B in segment s use b_gs[s].
  * out [M, ldo] bf16, ldo >= N, ldo % 8 == 0; only the [M, N] window is
  * written.  Each output element is one fp32 sum in a fixed k order, so
- * repeated calls give identical results.
+ * repeated calls give identical results.  The kernel's waits are bounded (2 s);
+ * without a workspace there is no place to report one that gave up: outputs
+ * may then be left unwritten.
  * Constraints: M >= 1, N % 128 == 0, K % 64 == 0, 1 <= nseg <= 4. */
 int nvfp4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, const float *a_gs, int64_t M,
                const uint8_t *b_codes, const uint8_t *b_scales, const float *b_gs,
@@ -452,8 +454,10 @@ int nvfp4_debug_gemv_timeout(const uint16_t *x, int64_t M, int64_t ldx,
  *                        1 at perfect balance; callers weight and add them)
  * A logit of -inf has p = 0 (a row of -inf alone: p = 0 everywhere), and so
  * has, for sigmoids, one below -1e30; other rows have their shares however low
- * the logits are.  Logits must not be NaN or +inf.  Sums are fp32 within a chunk of tokens and 64 bits
- * over the chunks, in a fixed order.  The workspace (caller-owned,
+ * the logits are.  Logits must not be NaN or +inf.  Sums of p are fp32 over a
+ * chunk of tokens and 64 bits over the chunks (a short batch is one chunk per
+ * sequence), the loss's are 64 bits; the order is fixed.  No output may overlap
+ * another or an input.  The workspace (caller-owned,
  * nvfp4_moe_balance_workspace_size bytes, 16-byte aligned, any contents) is
  * scratch: calls sharing one must not overlap on the device.  The size does not
  * shrink as T, S or E grow, so a workspace of the largest batch serves all.
@@ -472,7 +476,7 @@ int nvfp4_moe_balance(const float *logits, const int32_t *topk_ids, int64_t ld_i
  * counts are constants of the gradient, as ids are) and topk_weights the
  * renormalised weights of nvfp4_moe_topk over the row's slots that are not
  * skipped.  grad_loss [S] fp32; grad_weights [T, k] fp32 or NULL (no second
- * part); grad_logits [T, E] fp32, every row written: rows of padding and of
+ * part); grad_logits [T, E] fp32, apart from the inputs, every row written: rows of padding and of
  * tokens outside every sequence are 0.  Slots naming one expert twice add up.
  * Arguments and limits as for nvfp4_moe_balance.  One launch. */
 int nvfp4_moe_balance_backward(const float *logits, const int32_t *topk_ids, int64_t ld_ids, int64_t T, int E, int k,

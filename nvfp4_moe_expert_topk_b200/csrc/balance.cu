@@ -25,11 +25,15 @@
 // token's row, ids and weight gradients are loaded while the current one is
 // worked on.
 //
-// Measured (one B200, calls back to back): loss of 64 x 48 3.3 us, of 4096 x 384
-// in 7 sequences 7.7 us, of 65536 x 384 24.8 us (4.1 TB/s); gradient with weight
-// gradients of 4096 x 384 5.4 us, of 65536 x 384 46 us (4.4 TB/s).  The long ones
-// execute 173 and 380 instructions a token and warp (scores, sums, the slots'
-// part of the gradient) at 56 % of the issue rate.  Rows of 64 experts or fewer
+// Measured (one B200, per call in a CUDA graph of calls; softmax where nothing
+// else is said): loss of 64 x 48 3.3 us (sigmoid), of 4096 x 384 in 7 sequences
+// 7.6 us, of 65536 x 384 24.7 us (4.1 TB/s; sigmoid 27.2); gradient with weight
+// gradients of 4096 x 384 5.5 us (sigmoid), of 65536 x 384 46.4 us (4.4 TB/s;
+// sigmoid 48.7).  The long ones execute 173 and 380 instructions a token and warp
+// (scores, sums, the slots' part of the gradient) at 55 % of the issue rate, and
+// wait for loads (the largest stall) between them.  Rows of sigmoids that fp32
+// does not hold cost their warp a second pass: with one in a thousand 65536 x 384
+// takes 33 and 80 us, with nothing else 84 and 250.  Rows of 64 experts or fewer
 // leave half the lanes idle: 65536 x 48 takes 13.4 us and 24 us.
 #include "internal.h"
 #include "ptx.cuh"
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) balance_sum_kernel(const Balan
 
 // Gradient: one warp per token, consecutive tokens per warp.  The next kernel's
 // blocks come when this one's leave: they would take issue slots for nothing
-// (4096 x 384: 5.4 us, about 6.3 with an early trigger).
+// (4096 x 384: 5.5 us, about 6.4 with an early trigger).
 template <int P, bool V4, bool SIG>
 __global__ void __launch_bounds__(kThreads, backward_blocks(P)) balance_backward_kernel(const BalanceArgs a, int per_warp)
 {

@@ -42,10 +42,12 @@
 // in shared memory in a fixed order.  Every wait on a copy is bounded: a warp
 // that gives up stops loading, and the sums it has a share in become NaN.
 //
-// Measured (one B200, calls back to back): 3 x 200 x 256 (M x N x K) 3.3 us, 1 x
-// 2048 x 7168 6.9 us, 5 x 7168 x 8192 14.0 us (2.4 TB/s), 16 x 65536 x 1536 20.2
-// us (2.9 TB/s).  Of the last one 1 us is the launch, 5 us the x phase (loads, largest
-// exponents, conversion) and 12 us six steps per warp: 3900 cycles a step and
+// Measured (one B200, per call in a CUDA graph of calls): 3 x 200 x 256 (M x N x
+// K) 3.5 us, 1 x 2048 x 7168 7.0 us, 5 x 7168 x 8192 14.1 us (2.4 TB/s), 16 x
+// 65536 x 1536 20.5 us (2.9 TB/s); with bf16 operands in every block, the weights
+// in L2, 4.7, 9.0, 18.3 and 25.7 us instead of 3.6, 7.2, 13.3 and 18.4.  Of the
+// last one 1 us is the launch, 5 us the x phase (loads, largest and smallest
+// magnitudes, conversion) and 12 us six steps per warp: 3900 cycles a step and
 // scheduler, of which its 3.5 warps' conversions, products and MMAs take 2000
 // each at the rates measured alone (2.25, 2 and 8 cycles an instruction).
 // More warps (20, 24), another order of the loop's parts or more accumulators
